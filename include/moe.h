@@ -470,6 +470,89 @@ MOE_API moe_status moe_backward(const moe_shape* shape, const void* x, const flo
                                 int32_t* err_flag, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* Norms before and after the block, fused with the combine, a gate and the
+ * scaled residual ("PhiMoE in Transformers", section 2: layer norms with
+ * weight and bias around the sparse block; GraniteMoeSWA decoder layer: RMS
+ * norms, residual + hidden * residual_multiplier).
+ *
+ *   N(v) = (v - m) / sqrt(mean((v - m)^2) + eps) * weight + bias over the H
+ *   columns of a row, m = 0 (MOE_NORM_RMS) or mean(v) (MOE_NORM_LAYER);
+ *   MOE_NORM_NONE: N(v) = v (weight and bias NULL, eps ignored).
+ *   weight, bias: [H] float32 device pointers, NULL for ones / zeros.
+ *
+ * moe_norm_forward: y = N(x), x and y [T, H] dtype.
+ *
+ * moe_combine_norm: with v = moe_combine's sum for a token (float32, not
+ *   rounded),
+ *     h  = residual + scale * gate * N_post(v),     xn = N_next(h)
+ *   in one launch; h is rounded once when stored and xn comes from the
+ *   unrounded h.
+ *   residual [T, H] dtype or NULL (zero); gate [T] (MOE_GATE_TOKEN) or [H]
+ *   (MOE_GATE_CHANNEL) float32, NULL with MOE_GATE_NONE; post NULL = no norm;
+ *   next and xn_out both NULL = no next norm; y_out [T, H] dtype or NULL:
+ *   the combined v, rounded (what moe_norm_backward reads as x).
+ *   h_out may be residual itself; other outputs overlap nothing.
+ *
+ * moe_norm_backward: gradients of out = scale * gate * N(x) given dout:
+ *     dx [T, H] dtype (+ dadd [T, H] dtype when not NULL: the gradient that
+ *     reaches x past the norm), dweight [H], dbias [H], dgate [T] or [H]
+ *     float32 (each may be NULL; overwritten).  dx may be dout, dadd or x.
+ *   Row statistics are recomputed from x.  Deterministic.  Workspace:
+ *   moe_norm_backward_workspace_size() bytes, 16-byte aligned.
+ *
+ * All three use T, H, k, n_shared and dtype of `shape`, H <= 32768; slots
+ * whose entry of inv lies outside [0, T*k) (a plan with bad indices) add
+ * nothing.  float32 rows may have any H and alignment. */
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2 } moe_gate_kind;
+
+typedef struct {
+    int32_t kind;          /* moe_norm_kind */
+    float eps;             /* >= 0 */
+    const float* weight;   /* device, [H] or NULL */
+    const float* bias;     /* device, [H] or NULL */
+} moe_norm_spec;
+
+MOE_API moe_status moe_norm_forward(const moe_shape* shape, const moe_norm_spec* norm,
+                                    const void* x, void* y, void* stream);
+MOE_API moe_status moe_combine_norm(const moe_shape* shape, const void* y_slots,
+                                    const int32_t* inv, const void* residual,
+                                    const moe_norm_spec* post, int32_t gate_kind,
+                                    const float* gate, float scale, const moe_norm_spec* next,
+                                    void* y_out, void* h_out, void* xn_out, void* stream);
+MOE_API moe_status moe_norm_backward_workspace_size(const moe_shape* shape, size_t* bytes);
+MOE_API moe_status moe_norm_backward(const moe_shape* shape, const moe_norm_spec* norm,
+                                     const void* x, const void* dout, int32_t gate_kind,
+                                     const float* gate, float scale, const void* dadd, void* dx,
+                                     float* dweight, float* dbias, float* dgate, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* The global norm of a list of gradient tensors (moe_backward's and
+ * moe_norm_backward's, or any others) and clipping.
+ *   grads [n] host array of device pointers, numel [n] and dtype [n]
+ *   (moe_dtype) host arrays; dense tensors that do not overlap one another
+ *   (MOE_ERR_INVALID_ARG), each aligned to its element; numel 0 allowed.
+ * moe_grad_square_sum: total [1] float64 = the sum of g^2 over all tensors.
+ *   Ranks that hold different gradients all-reduce it (sum) before clipping.
+ * moe_clip_grads: norm [1] float32 (or NULL) = n = sqrt(total), and
+ *   g *= c with c = max_norm / (n + 1e-6) where c < 1; nothing is written to
+ *   the gradients when c >= 1.  As in the formula, an infinite norm zeroes
+ *   finite gradients and a NaN norm makes all of them NaN: read `norm`.
+ * moe_clip_grad_norm: both, on the tensors' own total (one launch less).
+ * Squares and sums are float64 in a fixed order (deterministic, no overflow
+ * of float32 squares).  Workspace: moe_grad_norm_workspace_size() bytes,
+ * 16-byte aligned. */
+MOE_API moe_status moe_grad_norm_workspace_size(size_t* bytes);
+MOE_API moe_status moe_grad_square_sum(int32_t n, void* const* grads, const int64_t* numel,
+                                       const int32_t* dtype, double* total, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+MOE_API moe_status moe_clip_grads(int32_t n, void* const* grads, const int64_t* numel,
+                                  const int32_t* dtype, const double* total, float max_norm,
+                                  float* norm, void* stream);
+MOE_API moe_status moe_clip_grad_norm(int32_t n, void* const* grads, const int64_t* numel,
+                                      const int32_t* dtype, float max_norm, float* norm,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* Diagnostic with no counterpart in the pages: runs the bounded pipeline wait
  * that every kernel here uses on an mbarrier nothing ever arrives on, so that
  * it expires after timeout_ns (0 < timeout_ns <= 10 s).  The kernel then ORs

@@ -11,3 +11,6 @@ from .moe import (MOE_BF16, MOE_F32, MoEError, MoEGraph, MoELayer, Shape,  # noq
                   load_library, permute, route, route_noaux_tc, route_permute, router_split,
                   shared_merge, train_state_size, workspace_size)
 from .expert_parallel import MoELayerEP, allreduce_partial, expert_range  # noqa: F401
+from .sublayer import (MoESublayer, Norm, alloc_grad_norm_workspace,  # noqa: F401
+                       alloc_norm_backward_workspace, clip_grad_norm, clip_grads, combine_norm,
+                       grad_square_sum, norm, norm_backward, norm_backward_workspace_size)

@@ -1,0 +1,200 @@
+// The global norm over a list of gradient tensors, and clipping.
+//
+//   n = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (n + 1e-6)),
+//   g *= c where c < 1
+// (the clipping step of a training loop, over the gradients that moe_backward
+// writes).  Squares are taken and summed in float64: the square of any float32
+// or bf16 value is a float64 in range, so neither gradients of 1e30 nor of
+// 1e-30 overflow or vanish, and the order of the sum is fixed: chunk by chunk
+// in each thread, threads in a tree, CTAs in order.  No atomics.
+//
+// Bound by memory: one read for the norm, one read and one write for the
+// scaling (nothing beyond the first read when the norm is within the limit).
+// The second pass walks the chunks backwards, so that it starts on what the
+// first pass left in L2.
+#include "grad_norm.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Tensor of a chunk (binary search over the prefix, in launch parameters).
+__device__ __forceinline__ int find_tensor(const GradList& l, int64_t chunk) {
+    int lo = 0, hi = l.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (l.chunk_start[mid] <= chunk) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ double square(float v) {
+    const double d = static_cast<double>(v);
+    return d * d;
+}
+
+__device__ __forceinline__ double square2(uint32_t w) {
+    return square(__uint_as_float(w << 16)) + square(__uint_as_float(w & 0xffff0000u));
+}
+
+// Sum over the CTA, in a fixed order; the result is in every thread.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double sh[kThreads / 32];
+    __shared__ double total;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double s = 0.0;
+        for (int i = 0; i < kThreads / 32; ++i) s += sh[i];
+        total = s;
+    }
+    __syncthreads();
+    return total;
+}
+
+// 16-byte vectors need an aligned base; a tensor that starts elsewhere (a view
+// into a larger buffer) goes value by value.
+__device__ __forceinline__ bool vector16(const void* p) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+__global__ void __launch_bounds__(kThreads) grad_square_sum_kernel(
+    const __grid_constant__ GradList l, bool add, double* part) {
+    pdl_launch_dependents();
+    pdl_wait();
+    double s = 0.0;
+    const int64_t chunks = l.chunk_start[l.n];
+    for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
+        const int i = find_tensor(l, ch);
+        const int64_t begin = (ch - l.chunk_start[i]) * l.chunk;
+        const int64_t left = l.numel[i] - begin;
+        const int n = static_cast<int>(left < l.chunk ? left : l.chunk);
+        int done = 0;
+        if (l.dtype[i] == MOE_F32) {
+            const float* g = static_cast<const float*>(l.ptr[i]) + begin;
+            if (vector16(g)) {
+                const float4* v = reinterpret_cast<const float4*>(g);
+                const int nv = n / 4;
+#pragma unroll 4
+                for (int j = threadIdx.x; j < nv; j += kThreads) {
+                    const float4 u = v[j];
+                    s += (square(u.x) + square(u.y)) + (square(u.z) + square(u.w));
+                }
+                done = nv * 4;
+            }
+            for (int j = done + threadIdx.x; j < n; j += kThreads) s += square(g[j]);
+        } else {
+            const uint16_t* g = static_cast<const uint16_t*>(l.ptr[i]) + begin;
+            if (vector16(g)) {
+                const uint4* v = reinterpret_cast<const uint4*>(g);
+                const int nv = n / 8;
+#pragma unroll 4
+                for (int j = threadIdx.x; j < nv; j += kThreads) {
+                    const uint4 u = v[j];
+                    s += (square2(u.x) + square2(u.y)) + (square2(u.z) + square2(u.w));
+                }
+                done = nv * 8;
+            }
+            for (int j = done + threadIdx.x; j < n; j += kThreads) s += square(bf16_to_f32(g[j]));
+        }
+    }
+    s = block_sum(s);
+    if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + s : s;
+}
+
+__device__ __forceinline__ double sum_parts(const double* part, int parts) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+    return block_sum(s);
+}
+
+__global__ void __launch_bounds__(kThreads) grad_total_kernel(const double* part, int parts,
+                                                              double* total) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const double s = sum_parts(part, parts);
+    if (threadIdx.x == 0) *total = s;
+}
+
+__device__ __forceinline__ uint32_t scale2(uint32_t w, float c) {
+    return pack_bf16x2(__uint_as_float(w << 16) * c, __uint_as_float(w & 0xffff0000u) * c);
+}
+
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradList l,
+                                                              const double* part, int parts,
+                                                              float max_norm, float* norm) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const double n2 = sqrt(sum_parts(part, parts));
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(n2);
+    const double ratio = static_cast<double>(max_norm) / (n2 + 1e-6);
+    if (ratio >= 1.0) return;            // a NaN norm goes on and reaches every gradient
+    const float c = static_cast<float>(ratio);
+    const int64_t chunks = l.chunk_start[l.n];
+    for (int64_t at = blockIdx.x; at < chunks; at += gridDim.x) {
+        const int64_t ch = chunks - 1 - at;
+        const int i = find_tensor(l, ch);
+        const int64_t begin = (ch - l.chunk_start[i]) * l.chunk;
+        const int64_t left = l.numel[i] - begin;
+        const int n = static_cast<int>(left < l.chunk ? left : l.chunk);
+        int done = 0;
+        if (l.dtype[i] == MOE_F32) {
+            float* g = static_cast<float*>(l.ptr[i]) + begin;
+            if (vector16(g)) {
+                float4* v = reinterpret_cast<float4*>(g);
+                const int nv = n / 4;
+#pragma unroll 4
+                for (int j = threadIdx.x; j < nv; j += kThreads) {
+                    float4 u = v[j];
+                    u.x *= c; u.y *= c; u.z *= c; u.w *= c;
+                    v[j] = u;
+                }
+                done = nv * 4;
+            }
+            for (int j = done + threadIdx.x; j < n; j += kThreads) g[j] *= c;
+        } else {
+            uint16_t* g = static_cast<uint16_t*>(l.ptr[i]) + begin;
+            if (vector16(g)) {
+                uint4* v = reinterpret_cast<uint4*>(g);
+                const int nv = n / 8;
+#pragma unroll 4
+                for (int j = threadIdx.x; j < nv; j += kThreads) {
+                    const uint4 u = v[j];
+                    v[j] = make_uint4(scale2(u.x, c), scale2(u.y, c), scale2(u.z, c),
+                                      scale2(u.w, c));
+                }
+                done = nv * 8;
+            }
+            for (int j = done + threadIdx.x; j < n; j += kThreads)
+                g[j] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_to_f32(g[j]) * c));
+        }
+    }
+}
+
+}  // namespace
+
+// part[0..parts) = (add ? part : 0) + the CTAs' sums of squares.
+cudaError_t launch_grad_square_sum(const GradList& l, bool add, double* part, int parts,
+                                   cudaStream_t st) {
+    return launch_pdl(grad_square_sum_kernel, dim3(parts), dim3(kThreads), 0, st, l, add, part);
+}
+
+cudaError_t launch_grad_total(const double* part, int parts, double* total, cudaStream_t st) {
+    return launch_pdl(grad_total_kernel, dim3(1), dim3(kThreads), 0, st, part, parts, total);
+}
+
+cudaError_t launch_grad_scale(const GradList& l, const double* part, int parts, float max_norm,
+                              float* norm, int num_sms, cudaStream_t st) {
+    const int64_t chunks = l.chunk_start[l.n];
+    int64_t grid = static_cast<int64_t>(num_sms) * 8;
+    if (grid > chunks) grid = chunks > 0 ? chunks : 1;
+    return launch_pdl(grad_scale_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st,
+                      l, part, parts, max_norm, norm);
+}
+
+}  // namespace moe

@@ -2,7 +2,7 @@
 // dispatch to the kernels.  No memory is allocated here.
 #include <cstring>
 
-#include "common.cuh"
+#include "host_common.cuh"
 
 namespace moe {
 cudaError_t launch_route(const moe_shape&, const void*, const float*, const float*, float*,
@@ -98,26 +98,7 @@ namespace {
 
 using moe::check_shape;
 
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-size_t elem_bytes(const moe_shape& s) { return s.dtype == MOE_BF16 ? 2 : 4; }
-
-int num_sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-    static int cached[64] = {0};
-    if (dev >= 0 && dev < 64 && cached[dev] > 0) return cached[dev];
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        n = 148;
-    if (dev >= 0 && dev < 64) cached[dev] = n;
-    return n;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+using namespace moe::host;
 
 struct Workspace {
     size_t permute_off, h_routed_off, h_shared_off, x_perm_off, inv_off;

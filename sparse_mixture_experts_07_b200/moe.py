@@ -23,7 +23,10 @@ EXPORTS = ("moe_status_str", "moe_workspace_size", "moe_route", "moe_permute", "
            "moe_combine", "moe_router_split_size", "moe_router_split", "moe_route_split",
            "moe_forward_mxfp4", "moe_forward_experts", "moe_combine_experts", "moe_cast_f32",
            "moe_route_noaux_tc", "moe_train_state_size", "moe_forward_train",
-           "moe_backward_workspace_size", "moe_backward", "moe_shared_merge")
+           "moe_backward_workspace_size", "moe_backward", "moe_shared_merge",
+           "moe_norm_forward", "moe_combine_norm", "moe_norm_backward_workspace_size",
+           "moe_norm_backward", "moe_grad_norm_workspace_size", "moe_grad_square_sum",
+           "moe_clip_grads", "moe_clip_grad_norm")
 
 
 class MoEShape(ctypes.Structure):
@@ -84,6 +87,15 @@ def load_library(path: str = LIB_PATH):
     lib.moe_backward_workspace_size.argtypes = [S, sz]
     lib.moe_backward.argtypes = [S, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_float, P,
                                  P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    f32 = ctypes.c_float
+    lib.moe_norm_forward.argtypes = [S, P, P, P, P]
+    lib.moe_combine_norm.argtypes = [S, P, P, P, P, i32, P, f32, P, P, P, P, P]
+    lib.moe_norm_backward_workspace_size.argtypes = [S, sz]
+    lib.moe_norm_backward.argtypes = [S, P, P, P, i32, P, f32, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.moe_grad_norm_workspace_size.argtypes = [sz]
+    lib.moe_grad_square_sum.argtypes = [i32, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.moe_clip_grads.argtypes = [i32, P, P, P, P, f32, P, P]
+    lib.moe_clip_grad_norm.argtypes = [i32, P, P, P, f32, P, P, ctypes.c_size_t, P]
     for f in EXPORTS[1:]:
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
@@ -491,7 +503,8 @@ class MoELayer:
             self.buf["logits"] = torch.empty(T, E, dtype=torch.float32, device=dev)
         self.last = None
 
-    def __call__(self, x, stream=None, y=None):
+    def slots(self, x, stream=None):
+        """The step up to the combine: (y_slots, inv), this layer's buffers."""
         s, b = self.shape, self.buf
         if self.routing is not None:
             idx, w, _ = route_noaux_tc(s, x, self.w_router, self.router_bias, self.routing[1],
@@ -515,9 +528,13 @@ class MoELayer:
             forward(s, x, offsets, perm, w, self.gate_up, self.down, self.sh_gate_up,
                     self.sh_down, self.workspace, self.err_flag, y_slots=b["y_slots"],
                     stream=stream)
-        out = combine(s, b["y_slots"], inv, y=b["y"] if y is None else y, stream=stream)
         self.last = b
-        return out
+        return b["y_slots"], inv
+
+    def __call__(self, x, stream=None, y=None):
+        y_slots, inv = self.slots(x, stream=stream)
+        return combine(self.shape, y_slots, inv, y=self.buf["y"] if y is None else y,
+                       stream=stream)
 
     def device_error(self) -> int:
         """Device-detected error bits (synchronises)."""
