@@ -470,6 +470,43 @@ MOE_API moe_status moe_backward(const moe_shape* shape, const void* x, const flo
                                 int32_t* err_flag, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* Experts in 8-bit floating point (OCP 8-bit Floating Point Specification,
+ * E4M3) with a scale per block of 128 along the contraction ("Mixture of
+ * Experts in Transformers", WeightConverter section: load-time conversions of
+ * packed expert weights).  A weight is code * s of its 128 x 128 block, an
+ * activation code * 2^e of its row's 128 columns, e the smallest integer with
+ * amax <= 448 * 2^e (at least -126); sums are float32:
+ *     g, u = x Wg^T, x Wu^T;  h = silu(g) * u, rounded like x;
+ *     y = routed_scale * w * (h Wd^T), rounded once to bf16.
+ * A value that is not finite becomes the NaN code (and NaN outputs).
+ *
+ * moe_fp8_quantize: n matrices w [n, rows, cols] of `dtype` (moe_dtype) to
+ *   codes q [n, rows, cols] and scales s [n, ceil(rows/128), ceil(cols/128)]
+ *   float32: s = amax / 448 of the block (1 where all are zero, at least
+ *   2^-126), q = w / s rounded to nearest even.  cols a multiple of 16, w and
+ *   q 16-byte aligned (else MOE_ERR_UNSUPPORTED).
+ *
+ * moe_forward_fp8: moe_forward on such weights, for any T (a single token
+ *   included).  Layouts as moe_forward with one byte per weight; scales (any
+ *   float32, as a checkpoint has them):
+ *     gate_up_s [E, 2, ceil(I/128), ceil(H/128)] (gate and up rows are blocked
+ *     separately), down_s [E, ceil(H/128), ceil(I/128)]; shared experts alike
+ *     (all NULL when n_shared == 0).
+ *   bf16 x and y_slots; H, I and I_shared multiples of 16; x, codes, y_slots
+ *   and the workspace 16-byte aligned; otherwise MOE_ERR_UNSUPPORTED.
+ *   Workspace: moe_fp8_workspace_size() bytes (moe_permute needs its own). */
+MOE_API moe_status moe_fp8_quantize(int64_t n, int32_t rows, int32_t cols, const void* w,
+                                    int32_t dtype, uint8_t* q, float* s, void* stream);
+MOE_API moe_status moe_fp8_workspace_size(const moe_shape* shape, size_t* bytes);
+MOE_API moe_status moe_forward_fp8(const moe_shape* shape, const void* x, const int32_t* offsets,
+                                   const int32_t* perm, const float* topk_w,
+                                   const uint8_t* gate_up_q, const float* gate_up_s,
+                                   const uint8_t* down_q, const float* down_s,
+                                   const uint8_t* sh_gate_up_q, const float* sh_gate_up_s,
+                                   const uint8_t* sh_down_q, const float* sh_down_s,
+                                   void* y_slots, int32_t* err_flag, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Norms before and after the block, fused with the combine, a gate and the
  * scaled residual ("PhiMoE in Transformers", section 2: layer norms with
  * weight and bias around the sparse block; GraniteMoeSWA decoder layer: RMS

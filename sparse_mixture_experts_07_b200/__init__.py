@@ -14,3 +14,5 @@ from .expert_parallel import MoELayerEP, allreduce_partial, expert_range  # noqa
 from .sublayer import (MoESublayer, Norm, alloc_grad_norm_workspace,  # noqa: F401
                        alloc_norm_backward_workspace, clip_grad_norm, clip_grads, combine_norm,
                        grad_square_sum, norm, norm_backward, norm_backward_workspace_size)
+from .fp8 import (alloc_fp8_workspace, forward_fp8, fp8_experts, fp8_quantize,  # noqa: F401
+                  fp8_workspace_size)

@@ -26,7 +26,8 @@ EXPORTS = ("moe_status_str", "moe_workspace_size", "moe_route", "moe_permute", "
            "moe_backward_workspace_size", "moe_backward", "moe_shared_merge",
            "moe_norm_forward", "moe_combine_norm", "moe_norm_backward_workspace_size",
            "moe_norm_backward", "moe_grad_norm_workspace_size", "moe_grad_square_sum",
-           "moe_clip_grads", "moe_clip_grad_norm")
+           "moe_clip_grads", "moe_clip_grad_norm", "moe_fp8_quantize", "moe_fp8_workspace_size",
+           "moe_forward_fp8")
 
 
 class MoEShape(ctypes.Structure):
@@ -96,6 +97,10 @@ def load_library(path: str = LIB_PATH):
     lib.moe_grad_square_sum.argtypes = [i32, P, P, P, P, P, ctypes.c_size_t, P]
     lib.moe_clip_grads.argtypes = [i32, P, P, P, P, f32, P, P]
     lib.moe_clip_grad_norm.argtypes = [i32, P, P, P, f32, P, P, ctypes.c_size_t, P]
+    i64 = ctypes.c_int64
+    lib.moe_fp8_quantize.argtypes = [i64, i32, i32, P, i32, P, P, P]
+    lib.moe_fp8_workspace_size.argtypes = [S, sz]
+    lib.moe_forward_fp8.argtypes = [S] + [P] * 15 + [ctypes.c_size_t, P]
     for f in EXPORTS[1:]:
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
@@ -458,9 +463,12 @@ class MoELayer:
     """
 
     def __init__(self, shape: Shape, w_router, router_bias, gate_up=None, down=None,
-                 sh_gate_up=None, sh_down=None, mxfp4=None, routing=None, merge_shared=True):
-        """Expert weights either as gate_up / down (dtype of `shape`), or as
-        `mxfp4` = {gate_up_q, gate_up_s, down_q, down_s} (decode batches).
+                 sh_gate_up=None, sh_down=None, mxfp4=None, routing=None, merge_shared=True,
+                 fp8=None):
+        """Expert weights either as gate_up / down (dtype of `shape`), as
+        `mxfp4` = {gate_up_q, gate_up_s, down_q, down_s} (decode batches), or as
+        `fp8`, an E4M3 expert set (fp8_experts; any batch, shared experts
+        inside it and not merged).
         `routing`: None for top-k with a softmax over the selected k (the bias
         added to the logits), or ("noaux_tc", n_group, topk_group) for
         DeepSeek-V3 routing (the bias steers the selection only).
@@ -468,7 +476,10 @@ class MoELayer:
         as separate groups."""
         self.shape = shape
         self.mxfp4 = mxfp4
+        self.fp8 = fp8
         self.routing = routing
+        if fp8 is not None and (gate_up is not None or mxfp4 is not None):
+            raise ValueError("fp8 experts take the place of gate_up / down and mxfp4")
         if routing is not None and routing[0] != "noaux_tc":
             raise ValueError(f"unknown routing {routing!r}")
         self.w_router, self.router_bias = w_router, router_bias
@@ -476,7 +487,7 @@ class MoELayer:
         self.w_split = router_split(shape, w_router)
         self.gate_up, self.down = gate_up, down
         self.sh_gate_up, self.sh_down = sh_gate_up, sh_down
-        if merge_shared and shape.n_shared > 1 and mxfp4 is None:
+        if merge_shared and shape.n_shared > 1 and mxfp4 is None and fp8 is None:
             shape, self.sh_gate_up, self.sh_down = shared_merge(shape, sh_gate_up, sh_down)
             self.shape = shape
         # MXFP4 weights prepared once for the tensor-core kernel where it
@@ -485,8 +496,13 @@ class MoELayer:
         if (mxfp4 is not None and 1 <= shape.T <= 64 and shape.n_shared == 0
                 and shape.dtype == MOE_BF16):
             self.mx_prepared = mxfp4_prepare(shape, mxfp4)
-        dev = (gate_up if mxfp4 is None else mxfp4["gate_up_q"]).device
+        dev = (gate_up if gate_up is not None else (mxfp4 or fp8)["gate_up_q"]).device
         self.workspace = alloc_workspace(shape, dev)
+        if fp8 is not None:
+            from . import fp8 as fp8_calls
+            fp8_calls.check_fp8_experts(shape, fp8, dev)
+            self._forward_fp8 = fp8_calls.forward_fp8
+            self.fp8_workspace = fp8_calls.alloc_fp8_workspace(shape, dev)
         self.err_flag = torch.zeros(1, dtype=torch.int32, device=dev)
         T, k, E, H = shape.T, shape.k, shape.E, shape.H
         self.buf = {
@@ -524,6 +540,9 @@ class MoELayer:
         elif self.mxfp4 is not None:
             forward_mxfp4(s, x, offsets, perm, w, self.mxfp4, self.workspace, self.err_flag,
                           y_slots=b["y_slots"], stream=stream)
+        elif self.fp8 is not None:
+            self._forward_fp8(s, x, offsets, perm, w, self.fp8, self.fp8_workspace,
+                              self.err_flag, y_slots=b["y_slots"], stream=stream)
         else:
             forward(s, x, offsets, perm, w, self.gate_up, self.down, self.sh_gate_up,
                     self.sh_down, self.workspace, self.err_flag, y_slots=b["y_slots"],
