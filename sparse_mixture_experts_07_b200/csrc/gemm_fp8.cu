@@ -10,18 +10,16 @@
 // memory, 256 columns each, alternate: the tensor cores fill one while the
 // epilogue drains the other.
 //
-// A tile is 128 rows x 256 MMA columns per CTA.  Eight epilogue warps each own
-// 32 rows (their TMEM lanes) and half of the columns, 128 accumulators per
-// thread.  GEMM 1 (kSwiGLU): 128 gate and the matching 128 up columns, so one
-// tile holds a whole 128-column block of h: the two threads of a row exchange
-// their maxima through shared memory and h is rounded to E4M3 in the epilogue,
-// never stored wider.  GEMM 2 (kScaled): 256 columns of y, times the routing
-// weight.
+// A tile is 128 rows x 256 MMA columns.  Eight epilogue warps each own 32 rows
+// (their TMEM lanes) and half of the columns, 128 accumulators per thread.
+// GEMM 1 (kSwiGLU): 128 gate and the matching 128 up columns, so one tile
+// holds a whole 128-column block of h: the two threads of a row exchange their
+// maxima through shared memory and h is rounded to E4M3 in the epilogue, never
+// stored wider.  GEMM 2 (kScaled): 256 columns of y, times the routing weight.
 //
-// PAIR: two CTAs of a cluster compute 256 x 256 with cta_group::2, each
-// loading its own 128 rows of A and 128 of the 256 B rows; as in the bf16 pair
-// kernel, without its folded half tiles.  One CTA alone otherwise (128 x 256),
-// which wastes fewer rows on small groups.
+// CTA pairs (cta_group::2, 256 x 256), which the bf16 kernel uses, were built
+// and measured first: every buffer hand-over then crosses the cluster twice
+// per K-block, and the Mixtral-shaped layer took 3.87 ms against 2.15 ms.
 #include "fp8.cuh"
 #include "gemm_common.cuh"
 
@@ -35,13 +33,14 @@ constexpr int UMMA_K = 32;
 constexpr int TILE_BYTES = 128 * BK;       // 128 rows of A or of B: 16 KB
 constexpr int TMEM_COLS = 512;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + EPI_WARPS * 32;
-template <bool PAIR> struct Cfg {
-    static constexpr int B_TILES = PAIR ? 1 : 2;              // of 128 rows each, per CTA
-    static constexpr int STAGE_BYTES = TILE_BYTES * (1 + B_TILES);
-    static constexpr int STAGES = PAIR ? 6 : 4;               // 192 KB
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
-};
+// One warpgroup for the producer and MMA warps (two of its warps idle), two for
+// the epilogue; the epilogue's threads take the registers that the first does
+// not need: 128 x 56 + 256 x 224 = 384 x 168, what the block is launched with.
+constexpr int THREADS = 128 + EPI_WARPS * 32;
+constexpr int REGS_FEW = 56, REGS_MANY = 224;
+constexpr int STAGE_BYTES = 3 * TILE_BYTES;   // 128 rows of A, 2 x 128 of B
+constexpr int STAGES = 4;                     // 192 KB
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
 }  // namespace fp8g
 
 struct Fp8GemmParams {
@@ -62,19 +61,56 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
-__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
-}
-
 // Instruction descriptor, kind::f8f6f4: E4M3 A and B (format 0, K-major), fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Bounded wait that polls: the product buffers change hands every K-block, and
+// a suspended thread's wake-up would be on that path.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, uint64_t deadline_ns) {
+    for (uint32_t i = 1;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 255u) == 0 && global_ns() > deadline_ns) return false;
+    }
+}
+
+template <int N> __device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Waits for this thread's tensor-memory loads; `v` is in the operand list so
+// that no use of it can be moved above the wait.
+__device__ __forceinline__ void tmem_ld_wait_for(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                   "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                   "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                   "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                   "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
+
+// acc[AT .. AT + 32) += s * v.  (The packed two-float multiply-add was slower:
+// 348 us against 296 for a 8192 x 2048 x 4096 layer.)
+template <int AT> __device__ __forceinline__ void add_scaled(float (&acc)[128], float s,
+                                                             const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[AT + j] = fmaf(s, v[j], acc[AT + j]);
 }
 
 // Barrier of the 256 epilogue threads.
@@ -82,36 +118,31 @@ __device__ __forceinline__ void epilogue_sync() {
     asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-template <int EPI, bool PAIR, int MAXG>
+template <int EPI>
 __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     const __grid_constant__ CUtensorMap map_a_routed,
     const __grid_constant__ CUtensorMap map_a_shared,
     const __grid_constant__ CUtensorMap map_b_routed,
     const __grid_constant__ CUtensorMap map_b_shared, const Fp8GemmParams fp) {
     using namespace fp8g;
-    using C = Cfg<PAIR>;
-    constexpr int STAGES = C::STAGES, STAGE_BYTES = C::STAGE_BYTES;
-    constexpr int TILE_M = PAIR ? 2 * BM : BM;
     constexpr int n_cols_per_tile = (EPI == kSwiGLU) ? BN / 2 : BN;
     const GemmParams& p = fp.g;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ GroupTableT<MAXG> gt;
+    __shared__ GroupTable gt;
     __shared__ uint32_t tmem_base_sh;
     __shared__ uint32_t mag_sh[2][2][BM];       // [tile parity][column half][row]
 
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
-    uint64_t* full = bars;                 // [STAGES] even CTA: TMA bytes (of both CTAs)
+    uint64_t* full = bars;                 // [STAGES] TMA bytes of the stage
     uint64_t* empty = bars + STAGES;       // [STAGES] stage consumed
     uint64_t* tfull = bars + 2 * STAGES;   // [2]      K-block product ready
-    uint64_t* tempty = tfull + 2;          // [2]      even CTA: product read by every epilogue warp
+    uint64_t* tempty = tfull + 2;          // [2]      product read by every epilogue warp
     uint64_t* drain = tempty + 2;          // [1]      all MMAs complete
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-    const int worker = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
-    const int workers = PAIR ? static_cast<int>(n_clusters_x()) : static_cast<int>(gridDim.x);
+    const int worker = static_cast<int>(blockIdx.x), workers = static_cast<int>(gridDim.x);
     const uint64_t deadline = global_ns() + p.timeout_ns;
 
     pdl_launch_dependents();
@@ -125,11 +156,11 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], (PAIR ? 2 : 1) * EPI_WARPS);
+            mbar_init(&tempty[b], EPI_WARPS);
         }
         mbar_init(drain, 1);
         fence_barrier_init();
-        build_group_table(gt, p.E, p.S, p.T, TILE_M, p.n_tiles_routed, p.n_tiles_shared);
+        build_group_table(gt, p.E, p.S, p.T, BM, p.n_tiles_routed, p.n_tiles_shared);
         tma_prefetch_desc(&map_a_routed);
         tma_prefetch_desc(&map_b_routed);
         if (p.S > 0) {
@@ -138,118 +169,98 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
         }
     }
     if (warp == 1) {
-        if (PAIR) {
-            tmem_alloc_pair(&tmem_base_sh, TMEM_COLS);
-            tmem_relinquish_pair();
-        } else {
-            tmem_alloc(&tmem_base_sh, TMEM_COLS);
-            tmem_relinquish();
-        }
+        tmem_alloc(&tmem_base_sh, TMEM_COLS);
+        tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();    // both CTAs' barriers initialised before any remote use
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
     const int total = gt.total_tiles;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            const uint64_t pol_a = l2_policy_evict_last();
-            const uint64_t pol_b = l2_policy_evict_normal();
-            const uint32_t full_leader =
-                PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
-            int stage = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int tile = worker; tile < total && ok; tile += workers) {
-                const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, TILE_M);
-                const CUtensorMap* ma = c.routed ? &map_a_routed : &map_a_shared;
-                const CUtensorMap* mb = c.routed ? &map_b_routed : &map_b_shared;
-                const int K = c.routed ? p.K_routed : p.K_shared;
-                const int eidx = c.routed ? c.g : c.g - p.E;
-                // routed -> sorted slot rows; shared GEMM 1 -> token rows; shared
-                // GEMM 2 -> that expert's block of h
-                const int a_row =
-                    (EPI == kSwiGLU && !c.routed ? 0 : gt.row0[c.g]) + c.m0 + rank * BM;
-                const int b_row = eidx * (c.routed ? p.b_rows_routed : p.b_rows_shared) + c.n0;
-                const int second = EPI == kSwiGLU ? (c.routed ? p.half_routed : p.half_shared)
-                                                  : BN / 2;
-                const int num_kb = (K + BK - 1) / BK;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1u, deadline)) { ok = false; break; }
-                    uint8_t* sa = smem + stage * STAGE_BYTES;
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * STAGE_BYTES);
-                    const uint32_t bar = full_leader + stage * 8;
-                    if (PAIR) {
-                        tma_load_2d_pair_hint(sa, ma, bar, kb * BK, a_row, pol_a);
-                        tma_load_2d_pair_hint(sa + TILE_BYTES, mb, bar, kb * BK,
-                                              b_row + rank * second, pol_b);
-                    } else {
+    if (warp < 4) {
+        give_registers<REGS_FEW>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            if (lane == 0) {
+                int stage = 0;
+                uint32_t phase = 0;
+                uint32_t filled = 0, parity = 0;      // per stage: loaded at all, phase of the last load
+                bool ok = true;
+                for (int tile = worker; tile < total && ok; tile += workers) {
+                    const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, BM);
+                    const CUtensorMap* ma = c.routed ? &map_a_routed : &map_a_shared;
+                    const CUtensorMap* mb = c.routed ? &map_b_routed : &map_b_shared;
+                    const int K = c.routed ? p.K_routed : p.K_shared;
+                    const int eidx = c.routed ? c.g : c.g - p.E;
+                    // routed -> sorted slot rows; shared GEMM 1 -> token rows; shared
+                    // GEMM 2 -> that expert's block of h
+                    const int a_row = (EPI == kSwiGLU && !c.routed ? 0 : gt.row0[c.g]) + c.m0;
+                    const int b_row = eidx * (c.routed ? p.b_rows_routed : p.b_rows_shared) + c.n0;
+                    const int second = EPI == kSwiGLU ? (c.routed ? p.half_routed : p.half_shared)
+                                                      : BN / 2;
+                    const int num_kb = (K + BK - 1) / BK;
+                    for (int kb = 0; kb < num_kb; ++kb) {
+                        if (!mbar_wait(&empty[stage], phase ^ 1u, deadline)) { ok = false; break; }
+                        uint8_t* sa = smem + stage * STAGE_BYTES;
+                        mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
                         tma_load_2d(sa, ma, &full[stage], kb * BK, a_row);
                         tma_load_2d(sa + TILE_BYTES, mb, &full[stage], kb * BK, b_row);
-                        tma_load_2d(sa + 2 * TILE_BYTES, mb, &full[stage], kb * BK,
-                                    b_row + second);
+                        tma_load_2d(sa + 2 * TILE_BYTES, mb, &full[stage], kb * BK, b_row + second);
+                        filled |= 1u << stage;
+                        parity = (parity & ~(1u << stage)) | (phase << stage);
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     }
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
+                // no copy is in flight when the CTA ends
+                for (int s = 0; s < STAGES; ++s)
+                    if (filled >> s & 1u)
+                        ok &= mbar_wait(&full[s], parity >> s & 1u, deadline + 1000000000ull);
+                if (!ok) raise_error(p.err_flag, MOE_ERR_TIMEOUT);
             }
-            if (!ok) raise_error(p.err_flag, MOE_ERR_TIMEOUT);
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA (even CTA)
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(TILE_M, BN);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
-            bool ok = true;
-            for (int tile = worker; tile < total && ok; tile += workers) {
-                const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, TILE_M);
-                const int num_kb = ((c.routed ? p.K_routed : p.K_shared) + BK - 1) / BK;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!mbar_wait(&tempty[buf], buf_phase ^ 1u, deadline) ||
-                        !mbar_wait(&full[stage], phase, deadline)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-                    const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-                    const uint32_t sb = sa + TILE_BYTES;
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMA
+            if (lane == 0) {
+                constexpr uint32_t idesc = idesc_e4m3_f32(BM, BN);
+                int stage = 0, buf = 0;
+                uint32_t phase = 0, buf_phase = 0;
+                bool ok = true;
+                for (int tile = worker; tile < total && ok; tile += workers) {
+                    const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, BM);
+                    const int num_kb = ((c.routed ? p.K_routed : p.K_shared) + BK - 1) / BK;
+                    for (int kb = 0; kb < num_kb; ++kb) {
+                        if (!mbar_poll(&tempty[buf], buf_phase ^ 1u, deadline) ||
+                            !mbar_poll(&full[stage], phase, deadline)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+                        const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
+                        const uint32_t sb = sa + TILE_BYTES;
 #pragma unroll
-                    for (int kk = 0; kk < BK / UMMA_K; ++kk) {
-                        const uint64_t da = smem_desc_sw128(sa + kk * UMMA_K);
-                        const uint64_t db = smem_desc_sw128(sb + kk * UMMA_K);
-                        if (PAIR) umma_e4m3_pair(d, da, db, idesc, kk != 0 ? 1u : 0u);
-                        else umma_e4m3(d, da, db, idesc, kk != 0 ? 1u : 0u);
-                    }
-                    if (PAIR) {
-                        umma_commit_pair(&empty[stage], 0x3);
-                        umma_commit_pair(&tfull[buf], 0x3);
-                    } else {
+                        for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                            umma_e4m3(d, smem_desc_sw128(sa + kk * UMMA_K),
+                                      smem_desc_sw128(sb + kk * UMMA_K), idesc, kk != 0 ? 1u : 0u);
                         umma_commit(&empty[stage]);
                         umma_commit(&tfull[buf]);
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                        if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
                     }
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
                 }
+                if (!ok) raise_error(p.err_flag, MOE_ERR_TIMEOUT);
+                // every issued MMA completes before the tensor memory is released
+                umma_commit(drain);
+                if (!mbar_wait(drain, 0, deadline + 1000000000ull))
+                    raise_error(p.err_flag, MOE_ERR_TIMEOUT);
             }
-            if (!ok) raise_error(p.err_flag, MOE_ERR_TIMEOUT);
-            // every issued MMA completes before the tensor memory is released
-            if (PAIR) umma_commit_pair(drain, 0x1);
-            else umma_commit(drain);
-            if (!mbar_wait(drain, 0, deadline + 1000000000ull))
-                raise_error(p.err_flag, MOE_ERR_TIMEOUT);
         }
     } else {
         // ------------------------------------------------------------ epilogue
+        take_registers<REGS_MANY>();
         const int quarter = warp & 3;               // TMEM lane quarter of this warp
-        const int half = (warp - 2) >> 2;           // column half
+        const int half = (warp - 4) >> 2;           // column half
         const int row = quarter * 32 + lane;
-        const uint32_t tempty_leader =
-            PAIR ? mapa_shared(smem_u32(tempty), 0) : smem_u32(tempty);
         // first TMEM column of this thread's two runs of 64
         const int col0 = EPI == kSwiGLU ? 64 * half : 128 * half;
         const int col1 = EPI == kSwiGLU ? 128 + 64 * half : 128 * half + 64;
@@ -259,12 +270,12 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
         // epilogue barrier needs every warp) without waiting or storing
         bool ok = true;
         for (int tile = worker; tile < total; tile += workers) {
-            const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, TILE_M);
+            const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, BM);
             const int K = c.routed ? p.K_routed : p.K_shared;
             const int N = c.routed ? p.N_routed : p.N_shared;
             const int num_kb = (K + BK - 1) / BK;
             const int eidx = c.routed ? c.g : c.g - p.E;
-            const int m = c.m0 + rank * BM + row;
+            const int m = c.m0 + row;
             const bool valid = m < c.rows;
             const bool any = m - lane < c.rows;      // of this warp's rows
             const int64_t a_row =
@@ -284,62 +295,85 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                 sw0 = sw + (static_cast<int64_t>(eidx) * row_blocks + rb) * num_kb;
                 sw1 = sw0;
             }
-            float acc0[64], acc1[64];
+            float acc[128];          // [0, 64) the first run of 64 columns, [64, 128) the second
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc0[j] = acc1[j] = 0.f;
-            uint32_t bytes = 0;
+            for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+            // scales one step ahead: a word of four activation scales, and the
+            // weight scales of the next K-block
+            uint32_t word = sa[0], bytes = 0;
+            float w0 = sw0[0], w1 = sw1[0];
 #pragma unroll 1
             for (int kb = 0; kb < num_kb; ++kb) {
-                if ((kb & 3) == 0) bytes = sa[kb >> 2];
+                if ((kb & 3) == 0) {
+                    bytes = word;
+                    if (kb + 4 < num_kb) word = sa[(kb >> 2) + 1];
+                }
                 const float ea = e8m0_value(bytes & 0xffu);
                 bytes >>= 8;
-                const float s0 = ea * sw0[kb];
-                const float s1 = EPI == kSwiGLU ? ea * sw1[kb] : s0;
-                if (ok && !mbar_wait(&tfull[buf], buf_phase, deadline)) {
+                const float s0 = ea * w0, s1 = ea * w1;
+                if (kb + 1 < num_kb) {
+                    w0 = sw0[kb + 1];
+                    if (EPI == kSwiGLU) w1 = sw1[kb + 1];
+                    else w1 = w0;
+                }
+                if (ok && !mbar_poll(&tfull[buf], buf_phase, deadline)) {
                     raise_error(p.err_flag, MOE_ERR_TIMEOUT);
                     ok = false;
                 }
                 ok = __all_sync(0xffffffffu, ok);    // the loads below are the warp's
                 tc_fence_after();
-                if (any && ok) {
+                const bool work = any && ok;
+                float va[32], vb[32];
+                if (work) {
+                    // each load is in flight while the columns before it are added
                     const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                        static_cast<uint32_t>(buf * BN);
-#pragma unroll
-                    for (int cc = 0; cc < 64; cc += 32) {
-                        float v[32];
-                        tmem_ld32(t + col0 + cc, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) acc0[cc + j] = fmaf(s0, v[j], acc0[cc + j]);
-                    }
-#pragma unroll
-                    for (int cc = 0; cc < 64; cc += 32) {
-                        float v[32];
-                        tmem_ld32(t + col1 + cc, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) acc1[cc + j] = fmaf(s1, v[j], acc1[cc + j]);
-                    }
+                    tmem_ld32(t + col0, va);
+                    tmem_ld_wait_for(va);
+                    tmem_ld32(t + col0 + 32, vb);
+                    add_scaled<0>(acc, s0, va);
+                    tmem_ld_wait_for(vb);
+                    tmem_ld32(t + col1, va);
+                    add_scaled<32>(acc, s0, vb);
+                    tmem_ld_wait_for(va);
+                    tmem_ld32(t + col1 + 32, vb);
+                    add_scaled<64>(acc, s1, va);
+                    tmem_ld_wait_for(vb);
                 }
+                // the buffer is free once its last columns are in registers
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(tempty_leader + buf * 8);
-                    else mbar_arrive(&tempty[buf]);
-                }
+                if (lane == 0) mbar_arrive(&tempty[buf]);
+                if (work) add_scaled<96>(acc, s1, vb);
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
             }
             if (EPI == kSwiGLU) {
                 // h = silu(g) u, rounded to E4M3 with the scale of its 128 columns
                 const int n = c.n0 + 64 * half;
-                uint32_t mag = 0;
+                float top = 0.f;
 #pragma unroll
                 for (int j = 0; j < 64; ++j) {
-                    const float g = acc0[j];
-                    const float h = __fdividef(g, 1.f + __expf(-g)) * acc1[j];
-                    acc0[j] = nan_if_not_finite(n + j < N ? h : 0.f);
-                    mag = max(mag, finite_mag(acc0[j]));
+                    const float g = acc[j];
+                    acc[j] = __fdividef(g, 1.f + __expf(-g)) * acc[64 + j];
                 }
+                if (n + 64 > N) {            // columns past the end take no part
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        if (n + j >= N) acc[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 64; ++j) top = fmaxf(top, fabsf(acc[j]));   // skips NaN
+                if (top == __uint_as_float(0x7f800000u)) {
+                    // an infinity would saturate: a NaN instead, outside the maximum
+                    uint32_t mag = 0;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        mag = max(mag, finite_mag(acc[j]));
+                        acc[j] = nan_if_not_finite(acc[j]);
+                    }
+                    top = __uint_as_float(mag);
+                }
+                uint32_t mag = __float_as_uint(top);
                 mag_sh[parity][half][row] = mag;
                 epilogue_sync();
                 mag = max(mag, mag_sh[parity][half ^ 1][row]);
@@ -356,8 +390,8 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int j = 16 * v + 4 * e;
-                            o[e] = e4m3x4(acc0[j] * inv, acc0[j + 1] * inv, acc0[j + 2] * inv,
-                                          acc0[j + 3] * inv);
+                            o[e] = e4m3x4(acc[j] * inv, acc[j + 1] * inv, acc[j + 2] * inv,
+                                          acc[j + 3] * inv);
                         }
                         if (n + 16 * v < N)
                             *reinterpret_cast<uint4*>(out + 16 * v) =
@@ -384,9 +418,8 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                     uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int j = 8 * (v & 7) + 2 * e;
-                        o[e] = v < 8 ? pack_bf16x2(scale * acc0[j], scale * acc0[j + 1])
-                                     : pack_bf16x2(scale * acc1[j], scale * acc1[j + 1]);
+                        const int j = 8 * v + 2 * e;
+                        o[e] = pack_bf16x2(scale * acc[j], scale * acc[j + 1]);
                     }
                     if (n + 8 * v < N)
                         *reinterpret_cast<uint4*>(out + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -397,11 +430,9 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
 
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        if (PAIR) tmem_dealloc_pair(tmem_base, TMEM_COLS);
-        else tmem_dealloc(tmem_base, TMEM_COLS);
+        tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
@@ -421,42 +452,36 @@ bool make_map_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t co
            CUDA_SUCCESS;
 }
 
-template <int EPI, bool PAIR>
+template <int EPI>
 cudaError_t launch_gemm(const Fp8GemmParams& p, int64_t rows_routed, int num_sms,
                         const CUtensorMap& ar, const CUtensorMap& as, const CUtensorMap& br,
                         const CUtensorMap& bs, cudaStream_t st) {
-    using C = fp8g::Cfg<PAIR>;
-    constexpr int ctas = PAIR ? 2 : 1;
-    constexpr int tile_m = ctas * fp8g::BM;
+    using namespace fp8g;
     const GemmParams& g = p.g;
     // at most this many tiles: every group may end in a partial m-tile
-    const int64_t tiles = (ceil_div(rows_routed, tile_m) + (g.E < rows_routed ? g.E : rows_routed)) *
+    const int64_t tiles = (ceil_div(rows_routed, BM) + (g.E < rows_routed ? g.E : rows_routed)) *
                               g.n_tiles_routed +
-                          g.S * ceil_div(g.T, tile_m) * g.n_tiles_shared;
-    const int64_t workers = num_sms / ctas < tiles ? num_sms / ctas : tiles;
-    auto kern = grouped_gemm_fp8<EPI, PAIR, kMaxGroups>;
+                          g.S * ceil_div(g.T, BM) * g.n_tiles_shared;
+    auto kern = grouped_gemm_fp8<EPI>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::SMEM_BYTES);
+                                         SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(workers * ctas), 1, 1);
-    cfg.blockDim = dim3(fp8g::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, ar, as, br, bs, p);
+    // the register split assumes what the block is launched with
+    static const bool split_fits = [&] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kern) == cudaSuccess &&
+               a.numRegs * THREADS >= 128 * REGS_FEW + 256 * REGS_MANY;
+    }();
+    if (!split_fits) return cudaErrorLaunchOutOfResources;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)),
+                      dim3(THREADS), SMEM_BYTES, st, ar, as, br, bs, p);
 }
 
-template <bool PAIR>
-cudaError_t run_ffn(const moe_shape& s, const Fp8Operands& o, int num_sms, cudaStream_t st) {
+}  // namespace
+
+// The experts on the quantised rows o.xq / o.xs.
+cudaError_t launch_ffn_fp8(const moe_shape& s, const Fp8Operands& o, int num_sms,
+                           cudaStream_t st) {
     const int64_t Tk = s.T * s.k;
     const int S = s.n_shared, Is = S > 0 ? s.I_shared : s.I;
     CUtensorMap a1r, a1s, b1r, b1s, a2r, a2s, b2r, b2s;
@@ -484,7 +509,7 @@ cudaError_t run_ffn(const moe_shape& s, const Fp8Operands& o, int num_sms, cudaS
     g.S = S;
     g.k = s.k;
     g.routed_scale = s.routed_scale;
-    g.group_m = PAIR ? 16 : 8;
+    g.group_m = 8;
     g.err_flag = o.err_flag;
     g.timeout_ns = 4000000000ull;
 
@@ -506,7 +531,7 @@ cudaError_t run_ffn(const moe_shape& s, const Fp8Operands& o, int num_sms, cudaS
     p.sw_shared = o.sh_gate_up_s;
     p.hs_routed = o.hs;
     p.hs_shared = o.hs_sh;
-    cudaError_t e = launch_gemm<kSwiGLU, PAIR>(p, Tk, num_sms, a1r, a1s, b1r, b1s, st);
+    cudaError_t e = launch_gemm<kSwiGLU>(p, Tk, num_sms, a1r, a1s, b1r, b1s, st);
     if (e != cudaSuccess) return e;
 
     // GEMM 2: the slots' rows of y
@@ -521,18 +546,7 @@ cudaError_t run_ffn(const moe_shape& s, const Fp8Operands& o, int num_sms, cudaS
     p.sa_shared = o.hs_sh;
     p.sw_routed = o.down_s;
     p.sw_shared = o.sh_down_s;
-    return launch_gemm<kScaled, PAIR>(p, Tk, num_sms, a2r, a2s, b2r, b2s, st);
-}
-
-}  // namespace
-
-// The experts on the quantised rows o.xq / o.xs.
-cudaError_t launch_ffn_fp8(const moe_shape& s, const Fp8Operands& o, int num_sms,
-                           cudaStream_t st) {
-    constexpr int kPairMinRows = 256;    // average rows per expert for CTA pairs
-    if (s.T * s.k >= static_cast<int64_t>(kPairMinRows) * s.E)
-        return run_ffn<true>(s, o, num_sms, st);
-    return run_ffn<false>(s, o, num_sms, st);
+    return launch_gemm<kScaled>(p, Tk, num_sms, a2r, a2s, b2r, b2s, st);
 }
 
 }  // namespace moe
