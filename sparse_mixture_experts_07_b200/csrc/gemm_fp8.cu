@@ -113,6 +113,20 @@ template <int AT> __device__ __forceinline__ void add_scaled(float (&acc)[128], 
     for (int j = 0; j < 32; ++j) acc[AT + j] = fmaf(s, v[j], acc[AT + j]);
 }
 
+// 2^x and 1/x to within 2 units in the last place, results below 2^-126 flushed
+// to zero: one instruction each (__expf and a division handle subnormals, in
+// several more).
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Barrier of the 256 epilogue threads.
 __device__ __forceinline__ void epilogue_sync() {
     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -354,7 +368,7 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
 #pragma unroll
                 for (int j = 0; j < 64; ++j) {
                     const float g = acc[j];
-                    acc[j] = __fdividef(g, 1.f + __expf(-g)) * acc[64 + j];
+                    acc[j] = g * rcp_approx(1.f + exp2_approx(g * -1.44269504f)) * acc[64 + j];
                 }
                 if (n + 64 > N) {            // columns past the end take no part
 #pragma unroll
@@ -509,7 +523,7 @@ cudaError_t launch_ffn_fp8(const moe_shape& s, const Fp8Operands& o, int num_sms
     g.S = S;
     g.k = s.k;
     g.routed_scale = s.routed_scale;
-    g.group_m = 8;
+    g.group_m = 16;
     g.err_flag = o.err_flag;
     g.timeout_ns = 4000000000ull;
 
