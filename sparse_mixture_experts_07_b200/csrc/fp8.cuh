@@ -55,6 +55,21 @@ __device__ __forceinline__ float nan_if_not_finite(float v) {
     return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : v;
 }
 
+// Rounds 8 consecutive values of a 128-column block that 16 neighbouring lanes
+// hold (all 32 lanes call); `byte` is the block's E8M0 scale.
+__device__ __forceinline__ uint2 e4m3_block_piece(float (&v)[8], uint32_t& byte) {
+    uint32_t mag = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mag = max(mag, finite_mag(v[e]));
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
+    byte = e8m0_of(mag);
+    const float inv = e8m0_inverse(byte);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = nan_if_not_finite(v[e]) * inv;
+    return make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+}
+
 // Bytes per row of E8M0 scales: one per 128 columns, rows 16-byte aligned.
 __host__ __device__ inline int fp8_scale_ld(int cols) {
     return ((cols + kFp8Block - 1) / kFp8Block + 15) / 16 * 16;
@@ -83,12 +98,23 @@ struct Fp8Operands {
     uint8_t* hs;
     uint8_t* hq_sh;            // [S*T, Is]
     uint8_t* hs_sh;
+    // decode batches (fp8_is_decode)
+    float* h32;                // [T*k, I] SwiGLU outputs, then [S*T, Is]
+    int32_t* arrived;          // [E + S, ceil(max(I, Is)/128)] units that wrote their part of h
 };
+
+// Batches whose groups have at most 8 rows: the weight-streaming kernels.
+inline bool fp8_is_decode(const moe_shape& s) { return s.T <= 8; }
+inline int fp8_h_blocks(const moe_shape& s) {
+    const int I = s.n_shared > 0 && s.I_shared > s.I ? s.I_shared : s.I;
+    return (I + kFp8Block - 1) / kFp8Block;
+}
 
 cudaError_t launch_fp8_quantize_weights(const void* w, bool bf16, int64_t n, int rows, int cols,
                                         uint8_t* q, float* s, cudaStream_t);
 cudaError_t launch_fp8_quantize_rows(const moe_shape&, const Fp8Operands&, int num_sms,
                                      cudaStream_t);
 cudaError_t launch_ffn_fp8(const moe_shape&, const Fp8Operands&, int num_sms, cudaStream_t);
+cudaError_t launch_ffn_fp8_decode(const moe_shape&, const Fp8Operands&, int num_sms, cudaStream_t);
 
 }  // namespace moe

@@ -84,16 +84,19 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_weights_kernel(
 
 // Activations: row p < T*k is x of the token of sorted slot p, rows past them
 // (with shared experts) the T tokens in order.  16 lanes hold a row's 128
-// columns, 8 values each.
+// columns, 8 values each.  For a decode batch it also clears the counters that
+// decode_gate_up's units arrive on.
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(
     const uint4* __restrict__ x, const int32_t* __restrict__ perm, int64_t slots, int64_t rows,
-    int k, int H, uint8_t* __restrict__ xq, uint8_t* __restrict__ xs) {
+    int k, int H, uint8_t* __restrict__ xq, uint8_t* __restrict__ xs, int32_t* arrived,
+    int counters) {
     const int blocks = (H + kFp8Block - 1) / kFp8Block;
     const int ld = fp8_scale_ld(H), vec = H / 8;
     const int lane = threadIdx.x & 15;
     const int64_t total = rows * blocks;
     pdl_launch_dependents();
     pdl_wait();
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < counters; i += gridDim.x * 256) arrived[i] = 0;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
          i - (threadIdx.x >> 4) < total; i += static_cast<int64_t>(gridDim.x) * 16) {
         const int64_t row = i / blocks;
@@ -113,22 +116,14 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(
         const uint4 u = in ? x[token * vec + c] : make_uint4(0, 0, 0, 0);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
         float v[8];
-        uint32_t mag = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[2 * e] = __uint_as_float(w[e] << 16);
             v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-            mag = max(mag, max(finite_mag(v[2 * e]), finite_mag(v[2 * e + 1])));
         }
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
-        const uint32_t byte = e8m0_of(mag);
-        const float inv = e8m0_inverse(byte);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = nan_if_not_finite(v[e]) * inv;
-        if (in)
-            *reinterpret_cast<uint2*>(xq + row * H + c * 8) =
-                make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+        uint32_t byte;
+        const uint2 codes = e4m3_block_piece(v, byte);
+        if (in) *reinterpret_cast<uint2*>(xq + row * H + c * 8) = codes;
         if (lane == 0 && token >= 0) xs[row * ld + b] = static_cast<uint8_t>(byte);
     }
 }
@@ -157,7 +152,8 @@ cudaError_t launch_fp8_quantize_rows(const moe_shape& s, const Fp8Operands& o, i
     int64_t grid = (total + 15) / 16;
     if (grid > static_cast<int64_t>(num_sms) * 16) grid = static_cast<int64_t>(num_sms) * 16;
     return launch_pdl(fp8_quantize_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st,
-                      static_cast<const uint4*>(o.x), o.perm, slots, rows, s.k, s.H, o.xq, o.xs);
+                      static_cast<const uint4*>(o.x), o.perm, slots, rows, s.k, s.H, o.xq, o.xs, o.arrived,
+                      fp8_is_decode(s) ? (s.E + s.n_shared) * fp8_h_blocks(s) : 0);
 }
 
 }  // namespace moe
