@@ -98,16 +98,30 @@ struct Fp8Operands {
     uint8_t* hs;
     uint8_t* hq_sh;            // [S*T, Is]
     uint8_t* hs_sh;
-    // decode batches (fp8_is_decode)
-    float* h32;                // [T*k, I] SwiGLU outputs, then [S*T, Is]
-    int32_t* arrived;          // [E + S, ceil(max(I, Is)/128)] units that wrote their part of h
+    // small batches (fp8_is_split)
+    float* part;               // [SMs, 2, fp8_part_rows, 256] sums of partial tiles
+    int32_t* arrived;          // [tiles of both GEMMs] K-blocks whose sums are in part
 };
 
-// Batches whose groups have at most 8 rows: the weight-streaming kernels.
-inline bool fp8_is_decode(const moe_shape& s) { return s.T <= 8; }
-inline int fp8_h_blocks(const moe_shape& s) {
-    const int I = s.n_shared > 0 && s.I_shared > s.I ? s.I_shared : s.I;
-    return (I + kFp8Block - 1) / kFp8Block;
+// Batches whose K-blocks are shared out over the SMs rather than whole tiles:
+// few rows per expert, so that what takes the time is reading the weights, and
+// a tile's sums are small.
+inline bool fp8_is_split(const moe_shape& s) { return s.T <= 64; }
+// Rows of one tile of such a batch (a plan may give an expert every slot).
+inline int fp8_part_rows(const moe_shape& s) {
+    return static_cast<int>(s.T * s.k < 128 ? s.T * s.k : 128);
+}
+
+// At most this many tiles: every group may end in a partial m-tile.
+struct Fp8Tiles {
+    int64_t gate_up, down;
+};
+inline Fp8Tiles fp8_tiles(const moe_shape& s) {
+    const int64_t slots = s.T * s.k;
+    const int64_t m = (slots + 127) / 128 + (s.E < slots ? s.E : slots);
+    const int64_t ms = s.n_shared * ((s.T + 127) / 128);
+    const int64_t Is = s.n_shared > 0 ? s.I_shared : 0;
+    return {m * ((s.I + 127) / 128) + ms * ((Is + 127) / 128), (m + ms) * ((s.H + 255) / 256)};
 }
 
 cudaError_t launch_fp8_quantize_weights(const void* w, bool bf16, int64_t n, int rows, int cols,
@@ -115,6 +129,5 @@ cudaError_t launch_fp8_quantize_weights(const void* w, bool bf16, int64_t n, int
 cudaError_t launch_fp8_quantize_rows(const moe_shape&, const Fp8Operands&, int num_sms,
                                      cudaStream_t);
 cudaError_t launch_ffn_fp8(const moe_shape&, const Fp8Operands&, int num_sms, cudaStream_t);
-cudaError_t launch_ffn_fp8_decode(const moe_shape&, const Fp8Operands&, int num_sms, cudaStream_t);
 
 }  // namespace moe

@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_weights_kernel(
 
 // Activations: row p < T*k is x of the token of sorted slot p, rows past them
 // (with shared experts) the T tokens in order.  16 lanes hold a row's 128
-// columns, 8 values each.  For a decode batch it also clears the counters that
-// decode_gate_up's units arrive on.
+// columns, 8 values each.  For a small batch it also clears the counters on
+// which the GEMMs' partial tiles arrive.
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(
     const uint4* __restrict__ x, const int32_t* __restrict__ perm, int64_t slots, int64_t rows,
     int k, int H, uint8_t* __restrict__ xq, uint8_t* __restrict__ xs, int32_t* arrived,
@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(
     const int ld = fp8_scale_ld(H), vec = H / 8;
     const int lane = threadIdx.x & 15;
     const int64_t total = rows * blocks;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();     // after the wait: see the GEMM's prologue
     for (int i = blockIdx.x * 256 + threadIdx.x; i < counters; i += gridDim.x * 256) arrived[i] = 0;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
          i - (threadIdx.x >> 4) < total; i += static_cast<int64_t>(gridDim.x) * 16) {
@@ -149,11 +149,12 @@ cudaError_t launch_fp8_quantize_rows(const moe_shape& s, const Fp8Operands& o, i
                                      cudaStream_t st) {
     const int64_t slots = s.T * s.k, rows = slots + (s.n_shared > 0 ? s.T : 0);
     const int64_t total = rows * ((s.H + kFp8Block - 1) / kFp8Block);
+    const Fp8Tiles tiles = fp8_tiles(s);
     int64_t grid = (total + 15) / 16;
     if (grid > static_cast<int64_t>(num_sms) * 16) grid = static_cast<int64_t>(num_sms) * 16;
     return launch_pdl(fp8_quantize_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st,
                       static_cast<const uint4*>(o.x), o.perm, slots, rows, s.k, s.H, o.xq, o.xs, o.arrived,
-                      fp8_is_decode(s) ? (s.E + s.n_shared) * fp8_h_blocks(s) : 0);
+                      fp8_is_split(s) ? static_cast<int>(tiles.gate_up + tiles.down) : 0);
 }
 
 }  // namespace moe

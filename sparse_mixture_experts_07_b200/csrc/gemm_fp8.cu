@@ -51,6 +51,10 @@ struct Fp8GemmParams {
     const float* sw_shared;
     uint8_t* hs_routed;           // kSwiGLU: E8M0 scales of h
     uint8_t* hs_shared;
+    // SPLIT
+    float* part;                  // [workers, 2, part_rows, 256] sums of a worker's partial tiles
+    int part_rows;
+    int32_t* arrived;             // [tiles] K-blocks whose sums are in part
 };
 
 __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -132,18 +136,222 @@ __device__ __forceinline__ void epilogue_sync() {
     asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    return g * rcp_approx(1.f + exp2_approx(g * -1.44269504f)) * u;
+}
+
+// What a row of y is multiplied by (GEMM 2).  A plan with skipped slots (bad
+// expert index) leaves holes in perm.
+__device__ __forceinline__ float row_weight(const GemmParams& p, const TileCoord& c,
+                                            int64_t row) {
+    if (!c.routed) return 1.f;
+    const int64_t slot = p.perm[row];
+    return slot >= 0 && slot < p.T * p.k ? p.routed_scale * p.topk_w[slot] : 0.f;
+}
+
+// The tiles a CTA computes, in the order that its producer, MMA and epilogue
+// warps all walk.  Without SPLIT: every workers-th tile, whole.  With SPLIT:
+// the K-blocks of all tiles in a row, an equal share per CTA; a share may
+// begin and end inside a tile.
+struct Segment {
+    TileCoord c;
+    int tile, num_kb, kb0, kb1;     // K-blocks [kb0, kb1) of num_kb
+};
+
+template <int EPI, bool SPLIT> struct Walk {
+    const GroupTable& gt;
+    const GemmParams& p;
+    int worker, workers;
+    int kb_routed, kb_shared;       // K-blocks of a tile
+    int routed_tiles;
+    int share, longer;              // SPLIT: K-blocks per CTA, one more in the first `longer`
+    int pos, end;                   // SPLIT: K-blocks; else tiles
+    __device__ __forceinline__ Walk(const GroupTable& gt, const GemmParams& p)
+        : gt(gt), p(p), worker(blockIdx.x), workers(gridDim.x) {
+        kb_routed = (p.K_routed + fp8g::BK - 1) / fp8g::BK;
+        kb_shared = (p.K_shared + fp8g::BK - 1) / fp8g::BK;
+        routed_tiles = gt.tile_start[p.E];
+        if (SPLIT) {
+            const int blocks = first_block(gt.total_tiles);
+            share = blocks / workers;
+            longer = blocks - share * workers;
+            pos = begin_of(worker);
+            end = begin_of(worker + 1);
+        } else {
+            pos = worker;
+            end = gt.total_tiles;
+        }
+    }
+    // first K-block of a tile, numbered through all tiles
+    __device__ __forceinline__ int first_block(int tile) const {
+        return min(tile, routed_tiles) * kb_routed + max(tile - routed_tiles, 0) * kb_shared;
+    }
+    __device__ __forceinline__ int begin_of(int w) const { return w * share + min(w, longer); }
+    // CTA that computes K-block b
+    __device__ __forceinline__ int worker_of(int b) const {
+        const int in_longer = longer * (share + 1);
+        return b < in_longer ? b / (share + 1) : longer + (b - in_longer) / share;
+    }
+    __device__ __forceinline__ bool next(Segment& s) {
+        if (pos >= end) return false;
+        if (SPLIT) {
+            const int routed = routed_tiles * kb_routed;
+            s.tile = pos < routed ? pos / kb_routed : routed_tiles + (pos - routed) / kb_shared;
+            s.c = tile_coord(s.tile);
+            s.num_kb = s.c.routed ? kb_routed : kb_shared;
+            s.kb0 = pos - first_block(s.tile);
+            s.kb1 = min(s.num_kb, s.kb0 + (end - pos));
+            pos += s.kb1 - s.kb0;
+        } else {
+            s.tile = pos;
+            s.c = tile_coord(s.tile);
+            s.num_kb = s.kb1 = s.c.routed ? kb_routed : kb_shared;
+            s.kb0 = 0;
+            pos += workers;
+        }
+        return true;
+    }
+    __device__ __forceinline__ TileCoord tile_coord(int tile) const {
+        return decode_tile(gt, p, tile, EPI == kSwiGLU ? fp8g::BN / 2 : fp8g::BN, fp8g::BM);
+    }
+};
+
+// The group table, by one warp, 32 groups at a time.
+__device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p) {
+    const int lane = threadIdx.x & 31;
+    int start = 0;
+    for (int g0 = 0; g0 < p.E + p.S; g0 += 32) {
+        const int g = g0 + lane;
+        int rows = 0, row0 = 0;
+        if (g < p.E) {
+            row0 = p.offsets[g];
+            rows = max(p.offsets[g + 1] - row0, 0);
+        } else if (g < p.E + p.S) {
+            row0 = static_cast<int>((g - p.E) * p.T);
+            rows = static_cast<int>(p.T);
+        }
+        const int tiles = (rows + fp8g::BM - 1) / fp8g::BM *
+                          (g < p.E ? p.n_tiles_routed : p.n_tiles_shared);
+        int sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += v;
+        }
+        if (g < p.E + p.S) {
+            gt.rows[g] = rows;
+            gt.row0[g] = row0;
+            gt.tile_start[g] = start + sum - tiles;
+        }
+        start += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) {
+        gt.n_groups = p.E + p.S;
+        gt.tile_start[p.E + p.S] = gt.total_tiles = start;
+    }
+}
+
+// Rows of the operands of a tile.
+struct TileSource {
+    int a_row, b_row, b_row2;       // A; the two halves of B
+};
 template <int EPI>
+__device__ __forceinline__ TileSource tile_source(const GemmParams& p, const GroupTable& gt,
+                                                  const TileCoord& c) {
+    TileSource t;
+    const int eidx = c.routed ? c.g : c.g - p.E;
+    // routed -> sorted slot rows; shared GEMM 1 -> token rows; shared GEMM 2 ->
+    // that expert's block of h
+    t.a_row = (EPI == kSwiGLU && !c.routed ? 0 : gt.row0[c.g]) + c.m0;
+    t.b_row = eidx * (c.routed ? p.b_rows_routed : p.b_rows_shared) + c.n0;
+    t.b_row2 = t.b_row + (EPI == kSwiGLU ? (c.routed ? p.half_routed : p.half_shared)
+                                         : fp8g::BN / 2);
+    return t;
+}
+
+// Adds up the parts of a tile in the order of their K-blocks (whichever CTA
+// does it, the sum is the same) and writes the tile's rows, a warp per row.
+template <int EPI, bool SPLIT>
+__device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const Segment& sg,
+                                             const GroupTable& gt, const Fp8GemmParams& fp,
+                                             int warp) {
+    const GemmParams& p = fp.g;
+    const TileCoord& c = sg.c;
+    const int lane = threadIdx.x & 31;
+    const int N = c.routed ? p.N_routed : p.N_shared;
+    const int first = walk.first_block(sg.tile);
+    const int w0 = walk.worker_of(first), w1 = walk.worker_of(first + sg.num_kb - 1);
+    const int rows = min(c.rows - c.m0, fp8g::BM);
+    // this lane's columns of the tile: 4 of gate and of up, or twice 4 of y
+    const int ca = 4 * lane, cb = 128 + 4 * lane;
+    for (int r = warp; r < rows; r += fp8g::EPI_WARPS) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        for (int w = w0; w <= w1; w += 4) {
+            // four workers' parts in flight, added in order
+            float4 va[4], vb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                va[i] = vb[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (w + i > w1) continue;
+                const int begin = walk.begin_of(w + i);
+                const float* from = fp.part + ((static_cast<int64_t>(w + i) * 2 +
+                                                (begin <= first)) * fp.part_rows + r) * fp8g::BN;
+                va[i] = __ldcg(reinterpret_cast<const float4*>(from + ca));
+                vb[i] = __ldcg(reinterpret_cast<const float4*>(from + cb));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a.x += va[i].x; a.y += va[i].y; a.z += va[i].z; a.w += va[i].w;
+                b.x += vb[i].x; b.y += vb[i].y; b.z += vb[i].z; b.w += vb[i].w;
+            }
+        }
+        const int64_t orow = static_cast<int64_t>(gt.row0[c.g]) + c.m0 + r;
+        if (EPI == kSwiGLU) {
+            const int n = c.n0 + ca;
+            float h[4] = {silu_mul(a.x, b.x), silu_mul(a.y, b.y), silu_mul(a.z, b.z),
+                          silu_mul(a.w, b.w)};
+            uint32_t mag = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = n < N ? nan_if_not_finite(h[j]) : 0.f;
+                mag = max(mag, finite_mag(h[j]));
+            }
+            mag = __reduce_max_sync(0xffffffffu, mag);
+            const uint32_t byte = e8m0_of(mag);
+            const float inv = e8m0_inverse(byte);
+            if (n < N)
+                *reinterpret_cast<uint32_t*>(
+                    static_cast<uint8_t*>(c.routed ? p.out_routed : p.out_shared) + orow * N + n) =
+                    e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+            if (lane == 0)
+                (c.routed ? fp.hs_routed : fp.hs_shared)[orow * fp8_scale_ld(N) + c.n0 / 128] =
+                    static_cast<uint8_t>(byte);
+        } else {
+            const float s = row_weight(p, c, orow);
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out_routed) +
+                                 (orow + (c.routed ? 0 : p.out_row0_shared)) * N + c.n0;
+            if (c.n0 + ca < N)
+                *reinterpret_cast<uint2*>(out + ca) = make_uint2(pack_bf16x2(s * a.x, s * a.y),
+                                                                 pack_bf16x2(s * a.z, s * a.w));
+            if (c.n0 + cb < N)
+                *reinterpret_cast<uint2*>(out + cb) = make_uint2(pack_bf16x2(s * b.x, s * b.y),
+                                                                 pack_bf16x2(s * b.z, s * b.w));
+        }
+    }
+}
+
+template <int EPI, bool SPLIT>
 __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     const __grid_constant__ CUtensorMap map_a_routed,
     const __grid_constant__ CUtensorMap map_a_shared,
     const __grid_constant__ CUtensorMap map_b_routed,
     const __grid_constant__ CUtensorMap map_b_shared, const Fp8GemmParams fp) {
     using namespace fp8g;
-    constexpr int n_cols_per_tile = (EPI == kSwiGLU) ? BN / 2 : BN;
     const GemmParams& p = fp.g;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ GroupTable gt;
     __shared__ uint32_t tmem_base_sh;
+    __shared__ int last_sh;
     __shared__ uint32_t mag_sh[2][2][BM];       // [tile parity][column half][row]
 
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -156,14 +364,13 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     uint64_t* drain = tempty + 2;          // [1]      all MMAs complete
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int worker = static_cast<int>(blockIdx.x), workers = static_cast<int>(gridDim.x);
-    const uint64_t deadline = global_ns() + p.timeout_ns;
 
-    pdl_launch_dependents();
-    pdl_wait();
-    stage_offsets(gt.tile_start, p.offsets, p.E);
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    // Every kernel of this chain lets the next one start only after its own
+    // pdl_wait: what the kernels before the previous one wrote (the plan) and
+    // the weights are there already, so the table is built and the first weight
+    // tiles are loaded while the previous kernel still runs.
+    if (warp == 0) build_table(gt, p);
+    if (threadIdx.x == 32) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -174,7 +381,13 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
         }
         mbar_init(drain, 1);
         fence_barrier_init();
-        build_group_table(gt, p.E, p.S, p.T, BM, p.n_tiles_routed, p.n_tiles_shared);
+    }
+    __syncwarp();
+    if (warp == 1) {
+        tmem_alloc(&tmem_base_sh, TMEM_COLS);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 64) {
         tma_prefetch_desc(&map_a_routed);
         tma_prefetch_desc(&map_b_routed);
         if (p.S > 0) {
@@ -182,15 +395,12 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
             tma_prefetch_desc(&map_b_shared);
         }
     }
-    if (warp == 1) {
-        tmem_alloc(&tmem_base_sh, TMEM_COLS);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = tmem_base_sh;
-    const int total = gt.total_tiles;
+    Walk<EPI, SPLIT> walk(gt, p);
+    Segment sg;
 
     if (warp < 4) {
         give_registers<REGS_FEW>();
@@ -199,28 +409,45 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
             if (lane == 0) {
                 int stage = 0;
                 uint32_t phase = 0;
-                uint32_t filled = 0, parity = 0;      // per stage: loaded at all, phase of the last load
+                uint32_t filled = 0, parity = 0;   // per stage: loaded at all, phase of the last load
                 bool ok = true;
-                for (int tile = worker; tile < total && ok; tile += workers) {
-                    const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, BM);
-                    const CUtensorMap* ma = c.routed ? &map_a_routed : &map_a_shared;
-                    const CUtensorMap* mb = c.routed ? &map_b_routed : &map_b_shared;
-                    const int K = c.routed ? p.K_routed : p.K_shared;
-                    const int eidx = c.routed ? c.g : c.g - p.E;
-                    // routed -> sorted slot rows; shared GEMM 1 -> token rows; shared
-                    // GEMM 2 -> that expert's block of h
-                    const int a_row = (EPI == kSwiGLU && !c.routed ? 0 : gt.row0[c.g]) + c.m0;
-                    const int b_row = eidx * (c.routed ? p.b_rows_routed : p.b_rows_shared) + c.n0;
-                    const int second = EPI == kSwiGLU ? (c.routed ? p.half_routed : p.half_shared)
-                                                      : BN / 2;
-                    const int num_kb = (K + BK - 1) / BK;
-                    for (int kb = 0; kb < num_kb; ++kb) {
-                        if (!mbar_wait(&empty[stage], phase ^ 1u, deadline)) { ok = false; break; }
+                // the weight tiles of the first stages, before pdl_wait
+                int ahead = 0;
+                {
+                    Walk<EPI, SPLIT> first = walk;
+                    while (ahead < STAGES && first.next(sg)) {
+                        const TileSource src = tile_source<EPI>(p, gt, sg.c);
+                        const CUtensorMap* mb = sg.c.routed ? &map_b_routed : &map_b_shared;
+                        for (int kb = sg.kb0; kb < sg.kb1 && ahead < STAGES; ++kb, ++ahead) {
+                            uint8_t* sb = smem + ahead * STAGE_BYTES + TILE_BYTES;
+                            mbar_arrive_expect_tx(&full[ahead], STAGE_BYTES);
+                            tma_load_2d(sb, mb, &full[ahead], kb * BK, src.b_row);
+                            tma_load_2d(sb + TILE_BYTES, mb, &full[ahead], kb * BK, src.b_row2);
+                        }
+                    }
+                }
+                pdl_wait();
+                pdl_launch_dependents();
+                const uint64_t deadline = global_ns() + p.timeout_ns;
+                while (ok && walk.next(sg)) {
+                    const TileSource src = tile_source<EPI>(p, gt, sg.c);
+                    const CUtensorMap* ma = sg.c.routed ? &map_a_routed : &map_a_shared;
+                    const CUtensorMap* mb = sg.c.routed ? &map_b_routed : &map_b_shared;
+                    for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
                         uint8_t* sa = smem + stage * STAGE_BYTES;
-                        mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
-                        tma_load_2d(sa, ma, &full[stage], kb * BK, a_row);
-                        tma_load_2d(sa + TILE_BYTES, mb, &full[stage], kb * BK, b_row);
-                        tma_load_2d(sa + 2 * TILE_BYTES, mb, &full[stage], kb * BK, b_row + second);
+                        if (ahead > 0) {
+                            --ahead;
+                        } else {
+                            if (!mbar_wait(&empty[stage], phase ^ 1u, deadline)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+                            tma_load_2d(sa + TILE_BYTES, mb, &full[stage], kb * BK, src.b_row);
+                            tma_load_2d(sa + 2 * TILE_BYTES, mb, &full[stage], kb * BK,
+                                        src.b_row2);
+                        }
+                        tma_load_2d(sa, ma, &full[stage], kb * BK, src.a_row);
                         filled |= 1u << stage;
                         parity = (parity & ~(1u << stage)) | (phase << stage);
                         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -236,13 +463,13 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
             // ------------------------------------------------------------ MMA
             if (lane == 0) {
                 constexpr uint32_t idesc = idesc_e4m3_f32(BM, BN);
+                pdl_wait();
+                const uint64_t deadline = global_ns() + p.timeout_ns;
                 int stage = 0, buf = 0;
                 uint32_t phase = 0, buf_phase = 0;
                 bool ok = true;
-                for (int tile = worker; tile < total && ok; tile += workers) {
-                    const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, BM);
-                    const int num_kb = ((c.routed ? p.K_routed : p.K_shared) + BK - 1) / BK;
-                    for (int kb = 0; kb < num_kb; ++kb) {
+                while (ok && walk.next(sg)) {
+                    for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
                         if (!mbar_poll(&tempty[buf], buf_phase ^ 1u, deadline) ||
                             !mbar_poll(&full[stage], phase, deadline)) {
                             ok = false;
@@ -272,6 +499,8 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     } else {
         // ------------------------------------------------------------ epilogue
         take_registers<REGS_MANY>();
+        pdl_wait();
+        const uint64_t deadline = global_ns() + p.timeout_ns;
         const int quarter = warp & 3;               // TMEM lane quarter of this warp
         const int half = (warp - 4) >> 2;           // column half
         const int row = quarter * 32 + lane;
@@ -283,11 +512,10 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
         // after a wait that ran out, the loops still run to their end (the
         // epilogue barrier needs every warp) without waiting or storing
         bool ok = true;
-        for (int tile = worker; tile < total; tile += workers) {
-            const TileCoord c = decode_tile(gt, p, tile, n_cols_per_tile, BM);
-            const int K = c.routed ? p.K_routed : p.K_shared;
+        while (walk.next(sg)) {
+            const TileCoord& c = sg.c;
             const int N = c.routed ? p.N_routed : p.N_shared;
-            const int num_kb = (K + BK - 1) / BK;
+            const int num_kb = sg.num_kb;
             const int eidx = c.routed ? c.g : c.g - p.E;
             const int m = c.m0 + row;
             const bool valid = m < c.rows;
@@ -296,7 +524,7 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                 (EPI == kSwiGLU && !c.routed ? 0 : static_cast<int64_t>(gt.row0[c.g])) +
                 (valid ? m : c.rows - 1);
             const uint32_t* sa = reinterpret_cast<const uint32_t*>(
-                (c.routed ? fp.sa_routed : fp.sa_shared) + a_row * fp8_scale_ld(K));
+                (c.routed ? fp.sa_routed : fp.sa_shared) + a_row * fp8_scale_ld(c.routed ? p.K_routed : p.K_shared));
             // weight scales of the two runs: gate and up, or the same 128 columns
             const int row_blocks = (N + 127) / 128;
             const float* sw = c.routed ? fp.sw_routed : fp.sw_shared;
@@ -312,20 +540,20 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
             float acc[128];          // [0, 64) the first run of 64 columns, [64, 128) the second
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-            // scales one step ahead: a word of four activation scales, and the
+            // scales one step ahead: words of four activation scales, and the
             // weight scales of the next K-block
-            uint32_t word = sa[0], bytes = 0;
-            float w0 = sw0[0], w1 = sw1[0];
+            uint32_t word = sa[sg.kb0 >> 2];
+            uint32_t next_word = (sg.kb0 | 3) + 1 < sg.kb1 ? sa[(sg.kb0 >> 2) + 1] : 0;
+            float w0 = sw0[sg.kb0], w1 = sw1[sg.kb0];
 #pragma unroll 1
-            for (int kb = 0; kb < num_kb; ++kb) {
-                if ((kb & 3) == 0) {
-                    bytes = word;
-                    if (kb + 4 < num_kb) word = sa[(kb >> 2) + 1];
+            for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
+                const float ea = e8m0_value(word >> (8 * (kb & 3)) & 0xffu);
+                if ((kb & 3) == 3) {
+                    word = next_word;
+                    if (kb + 5 < sg.kb1) next_word = sa[(kb >> 2) + 2];
                 }
-                const float ea = e8m0_value(bytes & 0xffu);
-                bytes >>= 8;
                 const float s0 = ea * w0, s1 = ea * w1;
-                if (kb + 1 < num_kb) {
+                if (kb + 1 < sg.kb1) {
                     w0 = sw0[kb + 1];
                     if (EPI == kSwiGLU) w1 = sw1[kb + 1];
                     else w1 = w0;
@@ -361,15 +589,37 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                 if (work) add_scaled<96>(acc, s1, vb);
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
             }
+            if (SPLIT && sg.kb1 - sg.kb0 < num_kb) {
+                // a part of the tile: leave its sums (in the tile's columns), and
+                // finish the tile if all parts are now there
+                float* mine = fp.part + ((static_cast<int64_t>(walk.worker) * 2 + (sg.kb0 == 0)) *
+                                             fp.part_rows + row) * BN;
+                if (valid) {
+#pragma unroll
+                    for (int j = 0; j < 64; j += 4) {
+                        *reinterpret_cast<float4*>(mine + col0 + j) =
+                            make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                        *reinterpret_cast<float4*>(mine + col1 + j) = make_float4(
+                            acc[64 + j], acc[64 + j + 1], acc[64 + j + 2], acc[64 + j + 3]);
+                    }
+                }
+                __threadfence();
+                epilogue_sync();
+                if (threadIdx.x == 128) {
+                    const int n = sg.kb1 - sg.kb0;
+                    last_sh = atomicAdd(fp.arrived + sg.tile, n) + n == num_kb;
+                    __threadfence();
+                }
+                epilogue_sync();
+                if (last_sh && ok) finish_parts<EPI, SPLIT>(walk, sg, gt, fp, warp - 4);
+                continue;
+            }
             if (EPI == kSwiGLU) {
                 // h = silu(g) u, rounded to E4M3 with the scale of its 128 columns
                 const int n = c.n0 + 64 * half;
                 float top = 0.f;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    const float g = acc[j];
-                    acc[j] = g * rcp_approx(1.f + exp2_approx(g * -1.44269504f)) * acc[64 + j];
-                }
+                for (int j = 0; j < 64; ++j) acc[j] = silu_mul(acc[j], acc[64 + j]);
                 if (n + 64 > N) {            // columns past the end take no part
 #pragma unroll
                     for (int j = 0; j < 64; ++j)
@@ -417,14 +667,9 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                             static_cast<uint8_t>(byte);
                 }
             } else if (valid && ok) {
-                float scale = 1.f;
                 int64_t orow = static_cast<int64_t>(gt.row0[c.g]) + m;
-                if (c.routed) {
-                    const int64_t slot = p.perm[orow];
-                    scale = slot >= 0 && slot < p.T * p.k ? p.routed_scale * p.topk_w[slot] : 0.f;
-                } else {
-                    orow += p.out_row0_shared;
-                }
+                const float scale = row_weight(p, c, orow);
+                if (!c.routed) orow += p.out_row0_shared;
                 const int n = c.n0 + 128 * half;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out_routed) + orow * N + n;
 #pragma unroll
@@ -466,17 +711,12 @@ bool make_map_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t co
            CUDA_SUCCESS;
 }
 
-template <int EPI>
-cudaError_t launch_gemm(const Fp8GemmParams& p, int64_t rows_routed, int num_sms,
+template <int EPI, bool SPLIT>
+cudaError_t launch_gemm(const Fp8GemmParams& p, int64_t tiles, int num_sms,
                         const CUtensorMap& ar, const CUtensorMap& as, const CUtensorMap& br,
                         const CUtensorMap& bs, cudaStream_t st) {
     using namespace fp8g;
-    const GemmParams& g = p.g;
-    // at most this many tiles: every group may end in a partial m-tile
-    const int64_t tiles = (ceil_div(rows_routed, BM) + (g.E < rows_routed ? g.E : rows_routed)) *
-                              g.n_tiles_routed +
-                          g.S * ceil_div(g.T, BM) * g.n_tiles_shared;
-    auto kern = grouped_gemm_fp8<EPI>;
+    auto kern = grouped_gemm_fp8<EPI, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          SMEM_BYTES);
     if (e != cudaSuccess) return e;
@@ -487,8 +727,9 @@ cudaError_t launch_gemm(const Fp8GemmParams& p, int64_t rows_routed, int num_sms
                a.numRegs * THREADS >= 128 * REGS_FEW + 256 * REGS_MANY;
     }();
     if (!split_fits) return cudaErrorLaunchOutOfResources;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles < num_sms ? tiles : num_sms)),
-                      dim3(THREADS), SMEM_BYTES, st, ar, as, br, bs, p);
+    const int64_t grid = SPLIT || tiles > num_sms ? num_sms : tiles;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(THREADS), SMEM_BYTES, st, ar,
+                      as, br, bs, p);
 }
 
 }  // namespace
@@ -545,7 +786,15 @@ cudaError_t launch_ffn_fp8(const moe_shape& s, const Fp8Operands& o, int num_sms
     p.sw_shared = o.sh_gate_up_s;
     p.hs_routed = o.hs;
     p.hs_shared = o.hs_sh;
-    cudaError_t e = launch_gemm<kSwiGLU>(p, Tk, num_sms, a1r, a1s, b1r, b1s, st);
+    const Fp8Tiles tiles = fp8_tiles(s);
+    const bool split = fp8_is_split(s);
+    p.part = o.part;
+    p.part_rows = fp8_part_rows(s);
+    p.arrived = o.arrived;
+    cudaError_t e = split ? launch_gemm<kSwiGLU, true>(p, tiles.gate_up, num_sms, a1r, a1s, b1r,
+                                                       b1s, st)
+                          : launch_gemm<kSwiGLU, false>(p, tiles.gate_up, num_sms, a1r, a1s, b1r,
+                                                        b1s, st);
     if (e != cudaSuccess) return e;
 
     // GEMM 2: the slots' rows of y
@@ -560,7 +809,9 @@ cudaError_t launch_ffn_fp8(const moe_shape& s, const Fp8Operands& o, int num_sms
     p.sa_shared = o.hs_sh;
     p.sw_routed = o.down_s;
     p.sw_shared = o.sh_down_s;
-    return launch_gemm<kScaled>(p, Tk, num_sms, a2r, a2s, b2r, b2s, st);
+    p.arrived = o.arrived + tiles.gate_up;
+    return split ? launch_gemm<kScaled, true>(p, tiles.down, num_sms, a2r, a2s, b2r, b2s, st)
+                 : launch_gemm<kScaled, false>(p, tiles.down, num_sms, a2r, a2s, b2r, b2s, st);
 }
 
 }  // namespace moe
