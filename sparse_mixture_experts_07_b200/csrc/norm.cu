@@ -60,6 +60,25 @@ template <> struct RowIO<float, 1> {
     __device__ __forceinline__ static Raw zero() { return 0.f; }
 };
 
+// A load, zero when !ok.  The 16-byte forms are volatile PTX, so that a group of
+// them stays ahead of the arithmetic: all of the group are in flight together.
+__device__ __forceinline__ uint4 load_if(const uint4* p, bool ok) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@q ld.global.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p), "r"(static_cast<int>(ok)));
+    return v;
+}
+__device__ __forceinline__ float4 load_if(const float4* p, bool ok) {
+    const uint4 u = load_if(reinterpret_cast<const uint4*>(p), ok);
+    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                       __uint_as_float(u.w));
+}
+__device__ __forceinline__ float load_if(const float* p, bool ok) { return ok ? *p : 0.f; }
+
 // VEC float32 parameters of the columns of vector c.
 template <int VEC>
 __device__ __forceinline__ void load_params(const float* p, int c, float (&v)[VEC]) {
@@ -164,39 +183,46 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(const CombineNormPar
     const Raw* residual = static_cast<const Raw*>(p.residual);
     const int64_t routed = p.T * p.k;
     const int nrows = p.k + p.S;
+    const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();
+    // lane j holds the row of slot j, k + S <= 24 of them; the next token's are
+    // fetched while this one is worked on.  A plan with skipped slots (bad expert
+    // index) leaves holes: -1, a slot that adds nothing.
+    auto slot_row = [&](int64_t t) {
+        int64_t row = -1;
+        if (t < p.T && lane < p.k) {
+            row = p.inv[t * p.k + lane];
+            if (row >= routed) row = -1;
+        } else if (t < p.T && lane < nrows) {
+            row = routed + (lane - p.k) * p.T + t;
+        }
+        return row;
+    };
+    int64_t mine = slot_row(blockIdx.x);
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const int64_t rows = mine;
+        mine = slot_row(t + gridDim.x);
         float v[VPT][VEC];
         Raw res[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             const bool in = c < nvec;
-            res[i] = residual && in ? residual[t * nvec + c] : IO::zero();
+            res[i] = load_if(residual + t * nvec + c, residual && in);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-            // up to four rows' loads in flight at once, summed in row order
-            for (int j = 0; j < nrows; j += 4) {
-                Raw u[4];
+            // up to IN_FLIGHT rows' loads at once, summed in row order
+            constexpr int IN_FLIGHT = VPT == 1 ? 8 : 4;
+            for (int j = 0; j < nrows; j += IN_FLIGHT) {
+                Raw u[IN_FLIGHT];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    u[r] = IO::zero();
-                    if (j + r < nrows) {
-                        int64_t row;
-                        if (j + r < p.k) {
-                            // a plan with skipped slots (bad expert index) leaves
-                            // holes: such a slot adds nothing
-                            row = p.inv[t * p.k + j + r];
-                            if (row < 0 || row >= routed) continue;
-                        } else {
-                            row = routed + (j + r - p.k) * p.T + t;
-                        }
-                        if (in) u[r] = slots[row * nvec + c];
-                    }
+                for (int r = 0; r < IN_FLIGHT; ++r) {
+                    const int64_t row = __shfl_sync(0xffffffffu, rows, (j + r) & 31);
+                    u[r] = load_if(slots + row * nvec + c, in && j + r < nrows && row >= 0);
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
+                for (int r = 0; r < IN_FLIGHT; ++r) {
                     float a[VEC];
                     IO::unpack(u[r], a);
 #pragma unroll
@@ -244,45 +270,73 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(const CombineNormPar
 // an RMS norm needs one block-wide reduction per row, a layer norm two.
 //
 // Bound by memory: x, dout (and dadd) read once, dx written.  Each thread owns
-// the same columns in every row of its CTA and keeps their sums A and B in
-// registers; the next row's loads are issued before this row's reduction.
+// the same columns in every row of its CTA and keeps their weights and their
+// sums A and B in registers; the next row's loads are issued before this row's
+// reduction, and two CTAs share an SM so that one's loads and arithmetic fill
+// the other's barrier.  PLAIN: an RMS norm (or none) without a bias, which
+// needs two row sums instead of four and no B.
 // The partial sums of the CTAs are added in CTA order by the second kernel:
 // no atomics, the same result every time.
-template <typename T, int VEC, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormBackwardParams p) {
+template <typename T, int VEC, int VPT, int MAXT, bool PLAIN>
+__global__ void __launch_bounds__(MAXT, MAXT == 512 && VPT == 1 ? 2 : 1)
+    norm_backward_kernel(const NormBackwardParams p) {
     using IO = RowIO<T, VEC>;
     using Raw = typename IO::Raw;
+    constexpr int SUMS = PLAIN ? 2 : 4;
+    // more columns per thread than registers for their parameters: loaded per row
+    constexpr bool KEEP = VPT * VEC <= 8;
     __shared__ float red1[2][1][32];
-    __shared__ float red4[2][4][32];
+    __shared__ float red[2][SUMS][32];
     BlockSum<1> sum1{red1};
-    BlockSum<4> sum4{red4};
+    BlockSum<SUMS> sum{red};
     const int nvec = p.H / VEC;
     const Raw* X = static_cast<const Raw*>(p.x);
     const Raw* DO = static_cast<const Raw*>(p.dout);
     const Raw* DA = static_cast<const Raw*>(p.dadd);
     const bool has_norm = p.norm.kind != MOE_NORM_NONE;
-    const bool layer = p.norm.kind == MOE_NORM_LAYER;
+    const bool layer = !PLAIN && p.norm.kind == MOE_NORM_LAYER;
     const bool token = p.gate_kind == MOE_GATE_TOKEN, channel = p.gate_kind == MOE_GATE_CHANNEL;
     const float inv_h = 1.f / static_cast<float>(p.H);
     pdl_launch_dependents();
     pdl_wait();
-    float A[VPT][VEC], B[VPT][VEC];
     Raw xr[VPT], dr[VPT], ar[VPT];
     auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             const bool in = t < p.T && c < nvec;
-            xr[i] = in ? X[t * nvec + c] : IO::zero();
-            dr[i] = in ? DO[t * nvec + c] : IO::zero();
-            ar[i] = in && DA ? DA[t * nvec + c] : IO::zero();
+            xr[i] = load_if(X + t * nvec + c, in);
+            dr[i] = load_if(DO + t * nvec + c, in);
+            ar[i] = load_if(DA + t * nvec + c, in && DA);
         }
     };
+    fetch(blockIdx.x);
+    // weight times channel gate of vector c
+    auto load_wg = [&](int c, float (&w)[VEC]) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) w[e] = 1.f;
+        if (c >= nvec) return;
+        if (p.norm.weight) load_params<VEC>(p.norm.weight, c, w);
+        if (channel) {
+            float g[VEC];
+            load_params<VEC>(p.gate, c, g);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] *= g[e];
+        }
+    };
+    float kept[KEEP ? VPT : 1][VEC];
+    if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) load_wg(threadIdx.x + i * blockDim.x, kept[i]);
+    }
+    float A[VPT][VEC], B[PLAIN ? 1 : VPT][VEC];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) A[i][e] = B[i][e] = 0.f;
-    fetch(blockIdx.x);
+        for (int e = 0; e < VEC; ++e) {
+            A[i][e] = 0.f;
+            if (!PLAIN) B[i][e] = 0.f;
+        }
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         float x[VPT][VEC], d[VPT][VEC];
         Raw add[VPT];
@@ -293,6 +347,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormBackwardP
             add[i] = ar[i];
         }
         fetch(t + gridDim.x);
+        const float gt = token ? p.gate[t] : 1.f;
         if (layer) {
             float s[1] = {0.f};
 #pragma unroll
@@ -308,66 +363,48 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormBackwardP
                     if (static_cast<int>(threadIdx.x + i * blockDim.x) < nvec) x[i][e] -= m;
         }
         // row sums: xc^2, (w gate_c dout) xc, w gate_c dout, b dout
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        float s[SUMS];
+#pragma unroll
+        for (int n = 0; n < SUMS; ++n) s[n] = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= nvec) continue;
-            float w[VEC], g[VEC];
-            if (p.norm.weight) {
-                load_params<VEC>(p.norm.weight, c, w);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-            }
-            if (channel) {
-                load_params<VEC>(p.gate, c, g);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) w[e] *= g[e];
-            }
+            float w[VEC];
+            if (!KEEP) load_wg(c, w);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float wd = w[e] * d[i][e];
+                const float wd = (KEEP ? kept[KEEP ? i : 0][e] : w[e]) * d[i][e];
                 s[0] += x[i][e] * x[i][e];
                 s[1] += wd * x[i][e];
-                s[2] += wd;
+                if (!PLAIN) s[2] += wd;
             }
-            if (token && p.norm.bias) {
-                load_params<VEC>(p.norm.bias, c, g);
+            if (!PLAIN && token && p.norm.bias) {
+                load_params<VEC>(p.norm.bias, c, w);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) s[3] += g[e] * d[i][e];
+                for (int e = 0; e < VEC; ++e) s[3] += w[e] * d[i][e];
             }
         }
-        if (has_norm || token) sum4(s);
+        if (has_norm || token) sum(s);
         const float r = has_norm ? 1.f / sqrtf(s[0] * inv_h + p.norm.eps) : 1.f;
-        const float gt = token ? p.gate[t] : 1.f;
-        const float f = p.scale * gt;
-        const float mean_wd = layer ? s[2] * inv_h : 0.f;
+        const float f = p.scale * gt * r;
+        const float mean_wd = layer ? s[PLAIN ? 0 : 2] * inv_h : 0.f;
         const float proj = has_norm ? s[1] * inv_h * r * r : 0.f;   // times xc: xhat mean(wD xhat)
-        if (token && threadIdx.x == 0 && p.dgate) p.dgate[t] = p.scale * (r * s[1] + s[3]);
+        if (token && threadIdx.x == 0 && p.dgate)
+            p.dgate[t] = p.scale * (r * s[1] + (PLAIN ? 0.f : s[PLAIN ? 0 : 3]));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             if (c >= nvec) continue;
             float w[VEC], o[VEC], a[VEC];
-            if (p.norm.weight) {
-                load_params<VEC>(p.norm.weight, c, w);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-            }
-            if (channel) {
-                load_params<VEC>(p.gate, c, o);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) w[e] *= o[e];
-            }
+            if (!KEEP) load_wg(c, w);
             IO::unpack(add[i], a);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                o[e] = f * r * (w[e] * d[i][e] - mean_wd - proj * x[i][e]) + a[e];
-                const float G = gt * d[i][e];
-                A[i][e] += G * (x[i][e] * r);
-                B[i][e] += G;
+                const float wd = (KEEP ? kept[KEEP ? i : 0][e] : w[e]) * d[i][e];
+                o[e] = f * (wd - mean_wd - proj * x[i][e]) + a[e];
+                A[i][e] += gt * r * d[i][e] * x[i][e];
+                if (!PLAIN) B[i][e] += gt * d[i][e];
             }
             static_cast<Raw*>(p.dx)[t * nvec + c] = IO::pack(o);
         }
@@ -383,31 +420,33 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormBackwardP
             for (int q = 0; q < VEC / 4; ++q) {
                 reinterpret_cast<float4*>(pa)[c * (VEC / 4) + q] =
                     make_float4(A[i][4 * q], A[i][4 * q + 1], A[i][4 * q + 2], A[i][4 * q + 3]);
-                reinterpret_cast<float4*>(pa + p.H)[c * (VEC / 4) + q] =
-                    make_float4(B[i][4 * q], B[i][4 * q + 1], B[i][4 * q + 2], B[i][4 * q + 3]);
+                if constexpr (!PLAIN)
+                    reinterpret_cast<float4*>(pa + p.H)[c * (VEC / 4) + q] = make_float4(
+                        B[i][4 * q], B[i][4 * q + 1], B[i][4 * q + 2], B[i][4 * q + 3]);
             }
         } else {
             pa[c] = A[i][0];
-            pa[p.H + c] = B[i][0];
+            if constexpr (!PLAIN) pa[p.H + c] = B[i][0];
         }
     }
 }
 
 // The parameters' gradients from the CTAs' column sums: 32 columns per CTA,
-// 8 warps each adding every eighth partial row, then the warps in order.
-__global__ void __launch_bounds__(256) norm_params_kernel(const NormBackwardParams p, int parts) {
-    __shared__ float sh[2][8][32];
+// 32 warps each adding every 32nd partial row, then the warps in order.
+__global__ void __launch_bounds__(1024) norm_params_kernel(const NormBackwardParams p, int parts,
+                                                           bool plain) {
+    __shared__ float sh[2][32][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;
     pdl_launch_dependents();
     pdl_wait();
     float a = 0.f, b = 0.f;
     if (c < p.H) {
-#pragma unroll 4
-        for (int i = warp; i < parts; i += 8) {
+#pragma unroll 8
+        for (int i = warp; i < parts; i += 32) {
             const float* row = p.part + static_cast<int64_t>(i) * 2 * p.H;
             a += row[c];
-            b += row[p.H + c];
+            if (!plain) b += row[p.H + c];
         }
     }
     sh[0][warp][lane] = a;
@@ -416,7 +455,7 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const NormBackwardPara
     if (warp != 0 || c >= p.H) return;
     a = b = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 32; ++i) {
         a += sh[0][i][lane];
         b += sh[1][i][lane];
     }
@@ -454,18 +493,21 @@ cudaError_t run_combine_norm(const CombineNormParams& p, int num_sms, cudaStream
 template <typename T, int VEC, int VPT, int MAXT>
 cudaError_t run_norm_backward(const NormBackwardParams& p, int num_sms, cudaStream_t st) {
     const int threads = threads_for(p.H / VEC, VPT);
-    auto kern = norm_backward_kernel<T, VEC, VPT, MAXT>;
+    // without a bias neither db nor dgate needs the sums B
+    const bool plain = p.norm.kind != MOE_NORM_LAYER && !p.norm.bias && !p.dbias;
+    auto kern = plain ? norm_backward_kernel<T, VEC, VPT, MAXT, true>
+                      : norm_backward_kernel<T, VEC, VPT, MAXT, false>;
     const int grid = norm_backward_parts(p.T, p.H, num_sms);
     cudaError_t e = launch_pdl(kern, dim3(grid), dim3(threads), 0, st, p);
     if (e != cudaSuccess || !p.part) return e;
-    return launch_pdl(norm_params_kernel, dim3((p.H + 31) / 32), dim3(256), 0, st, p, grid);
+    return launch_pdl(norm_params_kernel, dim3((p.H + 31) / 32), dim3(1024), 0, st, p, grid, plain);
 }
 
 }  // namespace
 
 // Rows of partial column sums, one per CTA of the backward kernel.
 int norm_backward_parts(int64_t T, int H, int num_sms) {
-    const int64_t cap = static_cast<int64_t>(num_sms) * (H <= 1024 ? 8 : H <= 4096 ? 4 : 2);
+    const int64_t cap = static_cast<int64_t>(num_sms) * (H <= 1024 ? 8 : H <= 2048 ? 4 : 2);
     return static_cast<int>(T < cap ? (T > 0 ? T : 1) : cap);
 }
 
@@ -487,10 +529,12 @@ cudaError_t launch_combine_norm(const CombineNormParams& p, bool bf16, bool vec1
 cudaError_t launch_norm_backward(const NormBackwardParams& p, bool bf16, bool vec16, int num_sms,
                                  cudaStream_t st) {
     if (bf16) {
+        if (p.H <= 4096) return run_norm_backward<__nv_bfloat16, 8, 1, 512>(p, num_sms, st);
         if (p.H <= 8192) return run_norm_backward<__nv_bfloat16, 8, 1, 1024>(p, num_sms, st);
         return run_norm_backward<__nv_bfloat16, 8, 8, 512>(p, num_sms, st);
     }
     if (vec16) {
+        if (p.H <= 2048) return run_norm_backward<float, 4, 1, 512>(p, num_sms, st);
         if (p.H <= 4096) return run_norm_backward<float, 4, 1, 1024>(p, num_sms, st);
         return run_norm_backward<float, 4, 16, 512>(p, num_sms, st);
     }
