@@ -6,80 +6,125 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 512;
-
 // Weights: one CTA per 128 x 128 block of a matrix.
 //   s = amax|W| / 448 over the block's finite values (1 for a block of zeros,
 //   at least 2^-126), code = e4m3(W / s), the division correctly rounded.
-// Bound by memory: each value is read once, kept in registers over the CTA's
-// maximum, and its code written once.  A thread holds pieces of 16 columns
-// (bf16: two 16-byte loads, float32: four), so that a code store is 16 bytes.
+// Bound by memory: each value is read once, kept as it was read in registers
+// over the CTA's maximum, and its code written once.  A thread holds pieces of
+// 16 columns (bf16: four, of two 16-byte loads each; float32: two, of four), so
+// that a code store is 16 bytes and 1024 resident threads keep 128 KB of loads
+// in flight on an SM.
+template <typename T> struct QuantPiece;
+template <> struct QuantPiece<__nv_bfloat16> {
+    static constexpr int LOADS = 2, PIECES = 4;
+    // largest magnitude of the piece, NaN skipped, two values at a time
+    __device__ __forceinline__ static float top(const uint4 (&u)[2]) {
+        __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {u[h].x, u[h].y, u[h].z, u[h].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+        }
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    __device__ __forceinline__ static float value(const uint4 (&u)[2], int e) {
+        const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+        return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+};
+template <> struct QuantPiece<float> {
+    static constexpr int LOADS = 4, PIECES = 2;
+    __device__ __forceinline__ static float top(const uint4 (&u)[4]) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(value(u, e)));
+        return m;
+    }
+    __device__ __forceinline__ static float value(const uint4 (&u)[4], int e) {
+        const uint4& q = u[e / 4];
+        return __uint_as_float(e % 4 == 0 ? q.x : e % 4 == 1 ? q.y : e % 4 == 2 ? q.z : q.w);
+    }
+};
+
+// Maximum over the CTA.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t (&red)[32]) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    __syncthreads();                // the last use of red
+    if (threadIdx.x < 32) red[threadIdx.x] = 0;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, red[threadIdx.x & 31]);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) fp8_quantize_weights_kernel(
+__global__ void __launch_bounds__(1024 / QuantPiece<T>::PIECES, QuantPiece<T>::PIECES) fp8_quantize_weights_kernel(
     const T* __restrict__ w, int rows, int cols, int row_blocks, int col_blocks,
     uint8_t* __restrict__ q, float* __restrict__ s) {
-    constexpr int kPieces = 2;              // 128 rows x 8 pieces of 16 over 512 threads
-    __shared__ uint32_t red[kThreads / 32];
+    using P = QuantPiece<T>;
+    constexpr int THREADS = 1024 / P::PIECES;       // 128 rows x 8 pieces
+    __shared__ uint32_t red[32];
     const int64_t b = blockIdx.x;
     const int cb = static_cast<int>(b % col_blocks);
     const int rb = static_cast<int>(b / col_blocks % row_blocks);
     const int64_t n = b / col_blocks / row_blocks;
-    float v[kPieces][16];
-    int64_t at[kPieces];
-    uint32_t mag = 0;
+    uint4 raw[P::PIECES][P::LOADS];
+    int64_t at[P::PIECES];
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        const int piece = threadIdx.x + i * kThreads;
+    for (int i = 0; i < P::PIECES; ++i) {
+        const int piece = threadIdx.x + i * THREADS;
         const int r = rb * 128 + piece / 8, c = cb * 128 + piece % 8 * 16;
         at[i] = r < rows && c < cols ? (n * rows + r) * cols + c : -1;
+        const uint4* src = reinterpret_cast<const uint4*>(w + at[i]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[i][e] = 0.f;
-        if (at[i] < 0) continue;
-        if constexpr (sizeof(T) == 2) {
-            const uint4* src = reinterpret_cast<const uint4*>(w + at[i]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 u = src[h];
-                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[i][8 * h + 2 * e] = __uint_as_float(x[e] << 16);
-                    v[i][8 * h + 2 * e + 1] = __uint_as_float(x[e] & 0xffff0000u);
-                }
-            }
-        } else {
-            const float4* src = reinterpret_cast<const float4*>(w + at[i]);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const float4 u = src[h];
-                v[i][4 * h] = u.x; v[i][4 * h + 1] = u.y;
-                v[i][4 * h + 2] = u.z; v[i][4 * h + 3] = u.w;
-            }
-        }
+        for (int h = 0; h < P::LOADS; ++h)
+            raw[i][h] = at[i] >= 0 ? __ldg(src + h) : make_uint4(0, 0, 0, 0);
     }
+    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < P::PIECES; ++i) top = fmaxf(top, P::top(raw[i]));
+    uint32_t mag = __float_as_uint(top);
+    mag = block_max(mag, red);
+    const bool infinite = mag >= 0x7f800000u;
+    if (infinite) {                                 // infinities take no part in the scale
+        mag = 0;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mag = max(mag, finite_mag(v[i][e]));
-    mag = __reduce_max_sync(0xffffffffu, mag);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mag;
-    __syncthreads();
-    mag = __reduce_max_sync(0xffffffffu, red[threadIdx.x & (kThreads / 32 - 1)]);
+        for (int i = 0; i < P::PIECES; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mag = max(mag, finite_mag(P::value(raw[i], e)));
+        mag = block_max(mag, red);
+    }
     const float amax = __uint_as_float(mag);
     const float scale = mag == 0 ? 1.f : fmaxf(amax / kE4M3Max, 1.17549435e-38f);
     if (threadIdx.x == 0) s[b] = scale;
+    // The correctly rounded quotient from the correctly rounded reciprocal
+    // (Markstein, IBM J. Res. Dev. 34, 1990): q = w y, then q - (s q - w) y; the
+    // residual is exact as long as it cannot underflow.
+    const float y = 1.f / scale;
+    const bool by_reciprocal = !infinite && scale > 7.8886091e-31f;     // 2^-100
+    auto store = [&](auto quotient) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        if (at[i] < 0) continue;
-        uint32_t o[4];
+        for (int i = 0; i < P::PIECES; ++i) {
+            uint32_t o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            o[e] = e4m3x4(nan_if_not_finite(v[i][4 * e]) / scale,
-                          nan_if_not_finite(v[i][4 * e + 1]) / scale,
-                          nan_if_not_finite(v[i][4 * e + 2]) / scale,
-                          nan_if_not_finite(v[i][4 * e + 3]) / scale);
-        *reinterpret_cast<uint4*>(q + at[i]) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+            for (int e = 0; e < 4; ++e)
+                o[e] = e4m3x4(quotient(P::value(raw[i], 4 * e)),
+                              quotient(P::value(raw[i], 4 * e + 1)),
+                              quotient(P::value(raw[i], 4 * e + 2)),
+                              quotient(P::value(raw[i], 4 * e + 3)));
+            if (at[i] >= 0)
+                *reinterpret_cast<uint4*>(q + at[i]) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    };
+    if (by_reciprocal)
+        store([&](float x) {
+            const float t = x * y;
+            return fmaf(-fmaf(scale, t, -x), y, t);
+        });
+    else
+        store([&](float x) { return nan_if_not_finite(x) / scale; });
 }
 
 // Activations: row p < T*k is x of the token of sorted slot p, rows past them
@@ -137,10 +182,10 @@ cudaError_t launch_fp8_quantize_weights(const void* w, bool bf16, int64_t n, int
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     if (bf16)
-        fp8_quantize_weights_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(
+        fp8_quantize_weights_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
             static_cast<const __nv_bfloat16*>(w), rows, cols, rb, cb, q, s);
     else
-        fp8_quantize_weights_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(
+        fp8_quantize_weights_kernel<<<static_cast<unsigned>(blocks), 512, 0, st>>>(
             static_cast<const float*>(w), rows, cols, rb, cb, q, s);
     return cudaGetLastError();
 }
