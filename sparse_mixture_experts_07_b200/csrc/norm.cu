@@ -16,9 +16,13 @@
 // unrounded h).
 //
 // Bound by memory: (k + S + 1) rows read, 2 (3 with y) written.  One CTA owns
-// one row at a time, one 16-byte vector per thread up to H = 8192 (bf16), so
-// that 2048 resident threads keep about 8 rows' loads in flight on an SM and
-// the two block-wide sums of one row hide behind the loads of the others.
+// one row at a time; what hides a row's load latency and its block-wide sums is
+// the other CTAs of the SM, so registers are held to five CTAs of 256 threads:
+// two 16-byte vectors per thread and at most 8 loads in flight.  Measured on a
+// B200, 32768 tokens of 2048 columns, 6 + 1 slots (1.34 GB): 230 us, 0.90 of the
+// copy bandwidth.  One vector per thread: 260 us (twice the threads in every
+// barrier); 88 registers and two CTAs less: 316 us; rows copied to shared memory
+// two to four tokens ahead, two CTAs per SM: 303 us and more.
 #include "norm.cuh"
 
 namespace moe {
@@ -60,8 +64,7 @@ template <> struct RowIO<float, 1> {
     __device__ __forceinline__ static Raw zero() { return 0.f; }
 };
 
-// A load, zero when !ok.  The 16-byte forms are volatile PTX, so that a group of
-// them stays ahead of the arithmetic: all of the group are in flight together.
+// A load, zero when !ok: volatile PTX, so that a group of them stays ahead of the arithmetic: all of the group are in flight together.
 __device__ __forceinline__ uint4 load_if(const uint4* p, bool ok) {
     uint4 v;
     asm volatile(
@@ -77,7 +80,15 @@ __device__ __forceinline__ float4 load_if(const float4* p, bool ok) {
     return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
                        __uint_as_float(u.w));
 }
-__device__ __forceinline__ float load_if(const float* p, bool ok) { return ok ? *p : 0.f; }
+__device__ __forceinline__ float load_if(const float* p, bool ok) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t"
+        "@q ld.global.f32 %0, [%1];\n\t}"
+        : "=f"(v)
+        : "l"(p), "r"(static_cast<int>(ok)));
+    return v;
+}
 
 // VEC float32 parameters of the columns of vector c.
 template <int VEC>
@@ -126,8 +137,8 @@ template <int N> struct BlockSum {
 // of every sum).  The variance is taken about the mean, in a second sum, so
 // that rows far from zero lose nothing.
 template <int VEC, int VPT>
-__device__ __forceinline__ void normalise(float (&v)[VPT][VEC], const NormDev& n, int nvec, int H,
-                                          BlockSum<1>& sum) {
+__device__ __forceinline__ void normalise(float (&v)[VPT][VEC], const NormDev& n, int nvec,
+                                          float inv_h, BlockSum<1>& sum) {
     if (n.kind == MOE_NORM_NONE) return;
     float m = 0.f;
     if (n.kind == MOE_NORM_LAYER) {
@@ -137,7 +148,7 @@ __device__ __forceinline__ void normalise(float (&v)[VPT][VEC], const NormDev& n
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s[0] += v[i][e];
         sum(s);
-        m = s[0] / static_cast<float>(H);
+        m = s[0] * inv_h;
     }
     float q[1] = {0.f};
 #pragma unroll
@@ -150,7 +161,7 @@ __device__ __forceinline__ void normalise(float (&v)[VPT][VEC], const NormDev& n
         }
     }
     sum(q);
-    const float r = 1.f / sqrtf(q[0] / static_cast<float>(H) + n.eps);
+    const float r = rsqrtf(q[0] * inv_h + n.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
@@ -172,13 +183,15 @@ __device__ __forceinline__ void normalise(float (&v)[VPT][VEC], const NormDev& n
     }
 }
 
-template <typename T, int VEC, int VPT>
-__global__ void __launch_bounds__(1024) combine_norm_kernel(const CombineNormParams p) {
+template <typename T, int VEC, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 5 : MAXT == 512 ? 2 : 1)
+    combine_norm_kernel(const CombineNormParams p) {
     using IO = RowIO<T, VEC>;
     using Raw = typename IO::Raw;
     __shared__ float red[2][1][32];
     BlockSum<1> sum{red};
     const int nvec = p.H / VEC;
+    const float inv_h = 1.f / static_cast<float>(p.H);
     const Raw* slots = static_cast<const Raw*>(p.y_slots);
     const Raw* residual = static_cast<const Raw*>(p.residual);
     const int64_t routed = p.T * p.k;
@@ -202,36 +215,49 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(const CombineNormPar
     int64_t mine = slot_row(blockIdx.x);
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         const int64_t rows = mine;
-        mine = slot_row(t + gridDim.x);
         float v[VPT][VEC];
         Raw res[VPT];
+        mine = slot_row(t + gridDim.x);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
-            const bool in = c < nvec;
-            res[i] = load_if(residual + t * nvec + c, residual && in);
+            res[i] = load_if(residual + t * nvec + c, residual && c < nvec);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-            // up to IN_FLIGHT rows' loads at once, summed in row order
-            constexpr int IN_FLIGHT = VPT == 1 ? 8 : 4;
-            for (int j = 0; j < nrows; j += IN_FLIGHT) {
-                Raw u[IN_FLIGHT];
+        }
+        // up to IN_FLIGHT rows' loads at once, summed in row order
+        constexpr int LOADS = VEC == 1 ? 16 : 8;
+        constexpr int IN_FLIGHT = VPT < LOADS ? LOADS / VPT : 1;
+        for (int j = 0; j < nrows; j += IN_FLIGHT) {
+            Raw u[IN_FLIGHT][VPT];
 #pragma unroll
-                for (int r = 0; r < IN_FLIGHT; ++r) {
-                    const int64_t row = __shfl_sync(0xffffffffu, rows, (j + r) & 31);
-                    u[r] = load_if(slots + row * nvec + c, in && j + r < nrows && row >= 0);
+            for (int r = 0; r < IN_FLIGHT; ++r) {
+                const int64_t row = __shfl_sync(0xffffffffu, rows, (j + r) & 31);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int c = threadIdx.x + i * blockDim.x;
+                    u[r][i] = load_if(slots + row * nvec + c,
+                                      c < nvec && j + r < nrows && row >= 0);
                 }
+            }
 #pragma unroll
-                for (int r = 0; r < IN_FLIGHT; ++r) {
+            for (int r = 0; r < IN_FLIGHT; ++r)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
                     float a[VEC];
-                    IO::unpack(u[r], a);
+                    IO::unpack(u[r][i], a);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) v[i][e] += a[e];
                 }
-            }
-            if (p.y_out && in) static_cast<Raw*>(p.y_out)[t * nvec + c] = IO::pack(v[i]);
         }
-        normalise<VEC, VPT>(v, p.post, nvec, p.H, sum);
+        if (p.y_out) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                if (c < nvec) static_cast<Raw*>(p.y_out)[t * nvec + c] = IO::pack(v[i]);
+            }
+        }
+        normalise<VEC, VPT>(v, p.post, nvec, inv_h, sum);
         const float gt = p.gate_kind == MOE_GATE_TOKEN ? p.scale * p.gate[t] : p.scale;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -249,7 +275,7 @@ __global__ void __launch_bounds__(1024) combine_norm_kernel(const CombineNormPar
             if (p.h_out) static_cast<Raw*>(p.h_out)[t * nvec + c] = IO::pack(v[i]);
         }
         if (p.xn_out) {
-            normalise<VEC, VPT>(v, p.next, nvec, p.H, sum);
+            normalise<VEC, VPT>(v, p.next, nvec, inv_h, sum);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int c = threadIdx.x + i * blockDim.x;
@@ -386,7 +412,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 && VPT == 1 ? 2 : 1)
             }
         }
         if (has_norm || token) sum(s);
-        const float r = has_norm ? 1.f / sqrtf(s[0] * inv_h + p.norm.eps) : 1.f;
+        const float r = has_norm ? rsqrtf(s[0] * inv_h + p.norm.eps) : 1.f;
         const float f = p.scale * gt * r;
         const float mean_wd = layer ? s[PLAIN ? 0 : 2] * inv_h : 0.f;
         const float proj = has_norm ? s[1] * inv_h * r * r : 0.f;   // times xc: xhat mean(wD xhat)
@@ -481,10 +507,10 @@ template <typename K> int resident_ctas(K kern, int threads, int num_sms) {
 
 int threads_for(int nvec, int vpt) { return (((nvec + vpt - 1) / vpt) + 31) / 32 * 32; }
 
-template <typename T, int VEC, int VPT>
+template <typename T, int VEC, int VPT, int MAXT>
 cudaError_t run_combine_norm(const CombineNormParams& p, int num_sms, cudaStream_t st) {
     const int threads = threads_for(p.H / VEC, VPT);
-    auto kern = combine_norm_kernel<T, VEC, VPT>;
+    auto kern = combine_norm_kernel<T, VEC, VPT, MAXT>;
     const int64_t cap = p.T <= num_sms ? num_sms : resident_ctas(kern, threads, num_sms);
     return launch_pdl(kern, dim3(static_cast<unsigned>(p.T < cap ? p.T : cap)), dim3(threads), 0,
                       st, p);
@@ -515,15 +541,17 @@ int norm_backward_parts(int64_t T, int H, int num_sms) {
 cudaError_t launch_combine_norm(const CombineNormParams& p, bool bf16, bool vec16, int num_sms,
                                 cudaStream_t st) {
     if (bf16) {
-        if (p.H <= 8192) return run_combine_norm<__nv_bfloat16, 8, 1>(p, num_sms, st);
-        return run_combine_norm<__nv_bfloat16, 8, 4>(p, num_sms, st);
+        if (p.H <= 4096) return run_combine_norm<__nv_bfloat16, 8, 2, 256>(p, num_sms, st);
+        if (p.H <= 8192) return run_combine_norm<__nv_bfloat16, 8, 2, 512>(p, num_sms, st);
+        return run_combine_norm<__nv_bfloat16, 8, 4, 1024>(p, num_sms, st);
     }
     if (vec16) {
-        if (p.H <= 4096) return run_combine_norm<float, 4, 1>(p, num_sms, st);
-        return run_combine_norm<float, 4, 8>(p, num_sms, st);
+        if (p.H <= 2048) return run_combine_norm<float, 4, 2, 1024>(p, num_sms, st);
+        if (p.H <= 4096) return run_combine_norm<float, 4, 4, 1024>(p, num_sms, st);
+        return run_combine_norm<float, 4, 8, 1024>(p, num_sms, st);
     }
-    if (p.H <= 4096) return run_combine_norm<float, 1, 4>(p, num_sms, st);
-    return run_combine_norm<float, 1, 32>(p, num_sms, st);
+    if (p.H <= 4096) return run_combine_norm<float, 1, 4, 1024>(p, num_sms, st);
+    return run_combine_norm<float, 1, 32, 1024>(p, num_sms, st);
 }
 
 cudaError_t launch_norm_backward(const NormBackwardParams& p, bool bf16, bool vec16, int num_sms,
