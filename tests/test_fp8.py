@@ -357,3 +357,92 @@ def test_layer_graph_stream_and_sublayer(cuda_ok, T):
     assert rel_l2(xn2.double().cpu().numpy(), xr) <= 2.0 ** -8
     with pytest.raises(ValueError):
         moe.MoELayer(shape, wr, None, gu.cuda(), dn.cuda(), fp8=fp8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 2, 16, 63, 64, 65, 128])
+def test_batch_sizes_around_the_split(cuda_ok, T):
+    """Up to 64 tokens share K-blocks out over the SMs, tiles then being summed
+    from parts; a tile may also lie whole in one share."""
+    for H, I, E, k, S, Is in ((1280, 640, 6, 2, 1, 384), (256, 4096, 64, 6, 0, 0)):
+        args = _setup(T, H, I, E, k, S, Is, seed=T)
+        y = _run(*args)
+        assert rel_l2(y.double().cpu().numpy(), _oracle(*args)) <= TOL
+        assert torch.equal(_run(*args), y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [8, 64, 300])
+def test_every_slot_on_one_expert(cuda_ok, T):
+    """A plan may name one expert in all of a token's slots: more rows in a
+    group than tokens."""
+    k, E = 8, 16
+    shape, x, _, _, w, fp8 = _setup(T, 144, 272, E, k, 0, 0, seed=4)
+    perm = torch.arange(T * k, dtype=torch.int32)
+    offsets = torch.zeros(E + 1, dtype=torch.int32)
+    offsets[6:] = T * k
+    args = (shape, x, perm, offsets, w, fp8)
+    assert rel_l2(_run(*args).double().cpu().numpy(), _oracle(*args)) <= TOL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 100])
+def test_holes_in_the_plan(cuda_ok, T):
+    """Entries of perm outside the slots (a plan with a bad expert index) are
+    not followed; their rows get weight 0, the others are as without them."""
+    shape, x, perm, offsets, w, fp8 = _setup(T, 144, 272, 4, 2, 1, 64, seed=5)
+    y = _run(shape, x, perm, offsets, w, fp8)
+    holed = perm.clone()
+    holed[1], holed[3] = -7, T * 2
+    # the rows that holes leave unset in the workspace are whatever was there
+    ws = torch.zeros(moe.fp8_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    got = _run(shape, x, holed, offsets, w, fp8, workspace=ws)
+    keep = torch.ones(shape.slot_rows, dtype=torch.bool, device="cuda")
+    keep[[1, 3]] = False
+    assert torch.equal(got[keep], y[keep]) and not got[~keep].any()
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once(cuda_ok):
+    """Two calls in flight, each with a workspace and outputs of its own."""
+    cases = [_setup(48, 512, 384, 8, 2, 1, 256, seed=6), _setup(700, 512, 384, 4, 2, 0, 0, seed=7)]
+    want = [_run(*c) for c in cases]
+    dev = [[c[i].cuda() for i in (1, 3, 2, 4)] + [{n: t.cuda() for n, t in c[5].items()}]
+           for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for i, (c, d, st) in enumerate(zip(cases, dev, streams)):
+            outs[i].append(moe.forward_fp8(c[0], *d, stream=st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(cuda_ok):
+    """More than 2^32 values of x codes and of y_slots; rows at both ends and
+    in the middle against the oracle."""
+    T, H, I, E, k = 262200, 2048, 16, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(8)
+    cpu = torch.Generator().manual_seed(8)
+    shape = moe.Shape(T=T, H=H, I=I, E=E, k=k)
+    assert T * k * H > 1 << 32
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    fp8 = _experts(cpu, H, E, I)
+    # every token on every expert, in sorted order
+    perm = (torch.arange(T, device="cuda")[None, :] * k +
+            torch.arange(E, device="cuda")[:, None]).reshape(-1).to(torch.int32)
+    offsets = torch.arange(E + 1, device="cuda", dtype=torch.int32) * T
+    w = torch.rand(T, k, generator=g, device="cuda")
+    y = moe.forward_fp8(shape, x, offsets, perm, w, {n: t.cuda() for n, t in fp8.items()})
+    arrays = {n: (t.view(torch.uint8) if n.endswith("_q") else t).numpy() for n, t in fp8.items()}
+    for e in (0, 3, E - 1):
+        for t0 in (0, T // 2, T - 40):
+            rows = slice(t0, t0 + 40)
+            want = ref.expert(x[rows].double().cpu().numpy(), arrays["gate_up_q"][e],
+                              arrays["gate_up_s"][e], arrays["down_q"][e], arrays["down_s"][e])
+            want *= w[rows, e].double().cpu().numpy()[:, None]
+            got = y[e * T + t0:e * T + t0 + 40].double().cpu().numpy()
+            assert rel_l2(got, want) <= TOL + 2.0 ** -3 / np.sqrt(40 * I)

@@ -694,3 +694,58 @@ def test_sublayer_training_step(cuda_ok):
     assert abs(float(norm) - n) <= 2.0 ** -23 * n
     for p, w in zip(params, clipped):
         _close("clipped", _np(p), w, 5 * U * np.abs(w) + 1e-40)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(cuda_ok):
+    """Slot rows, norm rows and a gradient tensor of more than 2^32 bytes and
+    2^31 values: rows at both ends against the oracle, and sums in closed form."""
+    T, H, k = 132000, 2048, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    s = _shape(T, H, k)
+    assert T * k * H > 1 << 31
+    slots = torch.randn(T * k, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    inv = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32)
+    h, xn, _ = moe.combine_norm(s, slots, inv, post=moe.Norm("rms", 1e-5),
+                                next_norm=moe.Norm("layer", 1e-5))
+    for t in (0, 1, T // 2, T - 1):
+        y = sum(_np(slots[int(inv[t * k + j])]) for j in range(k))[None]
+        hr, xr = ref.residual_norm(y, None, dict(kind="rms", eps=1e-5), None, 1.0,
+                                   dict(kind="layer", eps=1e-5))
+        _close("h", _np(h[t:t + 1]), hr, 2.0 ** -8 * np.abs(hr) + 1e-5)
+        _close("xn", _np(xn[t:t + 1]), xr, 2.0 ** -8 * np.abs(xr) + 2e-5)
+    del slots, h, xn
+    T = 1050000
+    s = _shape(T, H)
+    assert T * H > 1 << 31
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    dout = torch.ones(T, H, device="cuda", dtype=torch.bfloat16)
+    got = moe.norm_backward(s, moe.Norm("layer", 1e-5, torch.ones(H, device="cuda"),
+                                        torch.zeros(H, device="cuda")), x, dout)
+    assert (got["bias"] == float(T)).all()          # sums of ones: exact in float32
+    for t in (0, T // 2, T - 1):
+        # a constant gradient of a layer norm with equal weights vanishes
+        assert got["x"][t].float().abs().max() <= 1e-5
+    del x, dout, got
+    n = (1 << 31) + 12345
+    grad = torch.full((n,), 2.0, device="cuda")
+    assert abs(float(moe.clip_grad_norm([grad], 1.0)) / (2 * n ** 0.5) - 1) <= 2.0 ** -23
+    want = 1.0 / n ** 0.5
+    assert abs(float(grad[0]) / want - 1) < 1e-6 and abs(float(grad[-1]) / want - 1) < 1e-6
+
+
+@pytest.mark.gpu
+def test_large_values_and_small_variance(cuda_ok):
+    """Rows whose mean is 1000 times their spread: the variance is taken about
+    the mean.  The input's own rounding is none (float32); x - m is off by about
+    70 roundings of |m|, so relative to the spread by 70 u 1000."""
+    T, H = 64, 1000
+    g = torch.Generator().manual_seed(2)
+    x = (torch.randn(T, H, generator=g) + 1000.0).cuda()
+    got = _np(moe.norm(_shape(T, H, dtype=torch.float32), moe.Norm("layer", 0.0), x))
+    want = ref.norm(_np(x), "layer", 0.0)
+    _close("xn", got, want, 128 * U * (np.abs(want) + 1000.0))
+    d = torch.randn(T, H, generator=g).cuda()
+    got = moe.norm_backward(_shape(T, H, dtype=torch.float32), moe.Norm("layer", 0.0), x, d)["x"]
+    want = ref.norm_backward(_np(x), _np(d), "layer", 0.0)["x"]
+    assert rel_l2(_np(got), want) < 1000 * 256 * U
