@@ -55,19 +55,35 @@ __device__ __forceinline__ float nan_if_not_finite(float v) {
     return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fffffffu) : v;
 }
 
-// Rounds 8 consecutive values of a 128-column block that 16 neighbouring lanes
-// hold (all 32 lanes call); `byte` is the block's E8M0 scale.
-__device__ __forceinline__ uint2 e4m3_block_piece(float (&v)[8], uint32_t& byte) {
-    uint32_t mag = 0;
+// Rounds 8 consecutive bf16 values of a 128-column block that 16 neighbouring
+// lanes hold (all 32 lanes call); `byte` is the block's E8M0 scale.
+__device__ __forceinline__ uint2 e4m3_block_piece(const uint4& u, uint32_t& byte) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t half_mask = threadIdx.x & 16 ? 0xffff0000u : 0x0000ffffu;
+    // the largest magnitude, two values at a time; NaN is skipped
+    __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mag = max(mag, finite_mag(v[e]));
+    for (int e = 0; e < 4; ++e) {
+        m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+        v[2 * e] = __uint_as_float(w[e] << 16);
+        v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+    uint32_t mag = __float_as_uint(fmaxf(__low2float(m), __high2float(m)));
+    mag = __reduce_max_sync(half_mask, mag);
+    if (mag >= 0x7f800000u) {            // an infinity: NaN, and outside the maximum
+        mag = 0;
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
+        for (int e = 0; e < 8; ++e) {
+            mag = max(mag, finite_mag(v[e]));
+            v[e] = nan_if_not_finite(v[e]);
+        }
+        mag = __reduce_max_sync(half_mask, mag);
+    }
     byte = e8m0_of(mag);
     const float inv = e8m0_inverse(byte);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = nan_if_not_finite(v[e]) * inv;
-    return make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+    return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                      e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
 }
 
 // Bytes per row of E8M0 scales: one per 128 columns, rows 16-byte aligned.
@@ -98,6 +114,7 @@ struct Fp8Operands {
     uint8_t* hs;
     uint8_t* hq_sh;            // [S*T, Is]
     uint8_t* hs_sh;
+    int32_t* inv;              // [T*k] sorted position of each slot (fp8_by_token)
     // small batches (fp8_is_split)
     float* part;               // [SMs, 2, fp8_part_rows, 256] sums of partial tiles
     int32_t* arrived;          // [tiles of both GEMMs] K-blocks whose sums are in part
@@ -107,6 +124,10 @@ struct Fp8Operands {
 // few rows per expert, so that what takes the time is reading the weights, and
 // a tile's sums are small.
 inline bool fp8_is_split(const moe_shape& s) { return s.T <= 64; }
+// Batches whose activations are rounded once per token rather than once per
+// slot, through the inverse permutation.
+inline bool fp8_by_token(const moe_shape& s) { return !fp8_is_split(s) && s.k + s.n_shared > 1; }
+
 // Rows of one tile of such a batch (a plan may give an expert every slot).
 inline int fp8_part_rows(const moe_shape& s) {
     return static_cast<int>(s.T * s.k < 128 ? s.T * s.k : 128);

@@ -8,7 +8,7 @@ namespace {
 using namespace moe::host;
 
 struct Fp8Layout {
-    size_t xq, xs, hq, hs, hq_sh, hs_sh, part, arrived, total;
+    size_t xq, xs, hq, hs, hq_sh, hs_sh, inv, part, arrived, total;
 };
 
 Fp8Layout fp8_layout(const moe_shape& s) {
@@ -30,6 +30,8 @@ Fp8Layout fp8_layout(const moe_shape& s) {
     off += align_up(ST * Is);
     l.hs_sh = off;
     off += align_up(ST * moe::fp8_scale_ld(static_cast<int>(Is)));
+    l.inv = off;
+    if (moe::fp8_by_token(s)) off += align_up(Tk * 4);
     l.part = l.arrived = off;
     if (moe::fp8_is_split(s)) {
         off += align_up(static_cast<size_t>(num_sms()) * 2 * moe::fp8_part_rows(s) * 256 * 4);
@@ -109,7 +111,8 @@ moe_status moe_forward_fp8(const moe_shape* shape, const void* x, const int32_t*
     const moe::Fp8Operands o{x, offsets, perm, topk_w, gate_up_q, gate_up_s, down_q, down_s,
                              sh_gate_up_q, sh_gate_up_s, sh_down_q, sh_down_s, y_slots, err_flag,
                              ws + l.xq, ws + l.xs, ws + l.hq, ws + l.hs, ws + l.hq_sh,
-                             ws + l.hs_sh, reinterpret_cast<float*>(ws + l.part),
+                             ws + l.hs_sh, reinterpret_cast<int32_t*>(ws + l.inv),
+                             reinterpret_cast<float*>(ws + l.part),
                              reinterpret_cast<int32_t*>(ws + l.arrived)};
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t e = moe::launch_fp8_quantize_rows(s, o, num_sms(), cs);

@@ -127,49 +127,102 @@ __global__ void __launch_bounds__(1024 / QuantPiece<T>::PIECES, QuantPiece<T>::P
         store([&](float x) { return nan_if_not_finite(x) / scale; });
 }
 
-// Activations: row p < T*k is x of the token of sorted slot p, rows past them
-// (with shared experts) the T tokens in order.  16 lanes hold a row's 128
-// columns, 8 values each.  For a small batch it also clears the counters on
-// which the GEMMs' partial tiles arrive.
-__global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(
-    const uint4* __restrict__ x, const int32_t* __restrict__ perm, int64_t slots, int64_t rows,
-    int k, int H, uint8_t* __restrict__ xq, uint8_t* __restrict__ xs, int32_t* arrived,
-    int counters) {
-    const int blocks = (H + kFp8Block - 1) / kFp8Block;
-    const int ld = fp8_scale_ld(H), vec = H / 8;
-    const int lane = threadIdx.x & 15;
-    const int64_t total = rows * blocks;
+// Activations: row p < T*k of xq is x of the token of sorted slot p, rows past
+// them (with shared experts) the T tokens in order.  A warp takes 8 blocks of
+// 128 columns of a row of x, 16 lanes a block with 8 values each, its four
+// loads in flight together.
+//   BY_TOKEN: once per token, written to each of its slots' rows (inv: the
+//     sorted position of each slot), for large batches: 16384 tokens x 2048
+//     columns with 6 + 1 rows each take 130 us slot by slot, the rounding being
+//     what bounds them.
+//   else: once per row, without the inverse permutation (one launch less), for
+//     small ones; also clears the counters on which their GEMMs' partial tiles
+//     arrive.
+constexpr int kRowLoads = 4;
+constexpr int kRowBlocks = 2 * kRowLoads;
+
+struct QuantRowsParams {
+    const uint4* x;
+    const int32_t* perm;
+    const int32_t* inv;
+    int64_t T, slots;
+    int k, S, H;
+    uint8_t* xq;
+    uint8_t* xs;
+    int32_t* arrived;
+    int counters;
+};
+
+template <bool BY_TOKEN>
+__global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantRowsParams p) {
+    const int blocks = (p.H + kFp8Block - 1) / kFp8Block;
+    const int per_row = (blocks + kRowBlocks - 1) / kRowBlocks;
+    const int ld = fp8_scale_ld(p.H), vec = p.H / 8;
+    const int lane = threadIdx.x & 15, half = threadIdx.x >> 4 & 1;
+    const int64_t total = (BY_TOKEN ? p.T : p.slots + (p.S > 0 ? p.T : 0)) * per_row;
     pdl_wait();
     pdl_launch_dependents();     // after the wait: see the GEMM's prologue
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < counters; i += gridDim.x * 256) arrived[i] = 0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-         i - (threadIdx.x >> 4) < total; i += static_cast<int64_t>(gridDim.x) * 16) {
-        const int64_t row = i / blocks;
-        const int b = static_cast<int>(i - row * blocks);
-        int64_t token = -1;
-        if (i < total) {
-            if (row < slots) {
-                const int64_t q = perm[row];
+    if (!BY_TOKEN)
+        for (int i = blockIdx.x * 256 + threadIdx.x; i < p.counters; i += gridDim.x * 256)
+            p.arrived[i] = 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < total;
+         i += static_cast<int64_t>(gridDim.x) * 8) {
+        const int64_t row = total <= 0xffffffffll
+                                ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per_row)
+                                : i / per_row;
+        const int first = static_cast<int>(i - row * per_row) * kRowBlocks + half;
+        int64_t token = row;
+        if (!BY_TOKEN) {
+            token = row - p.slots;
+            if (row < p.slots) {
+                const int32_t q = p.perm[row];
                 // a plan with skipped slots (bad expert index) leaves holes
-                if (q >= 0 && q < slots) token = q / k;
-            } else {
-                token = row - slots;
+                if (q < 0 || q >= p.slots) continue;
+                token = q / p.k;
             }
         }
-        const int c = b * 16 + lane;
-        const bool in = token >= 0 && c < vec;
-        const uint4 u = in ? x[token * vec + c] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float v[8];
+        uint4 u[kRowLoads];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        for (int n = 0; n < kRowLoads; ++n) {
+            const int c = (first + 2 * n) * 16 + lane;
+            u[n] = c < vec ? p.x[token * vec + c] : make_uint4(0, 0, 0, 0);
         }
-        uint32_t byte;
-        const uint2 codes = e4m3_block_piece(v, byte);
-        if (in) *reinterpret_cast<uint2*>(xq + row * H + c * 8) = codes;
-        if (lane == 0 && token >= 0) xs[row * ld + b] = static_cast<uint8_t>(byte);
+        uint2 codes[kRowLoads];
+        uint32_t byte[kRowLoads];
+#pragma unroll
+        for (int n = 0; n < kRowLoads; ++n) codes[n] = e4m3_block_piece(u[n], byte[n]);
+        auto write = [&](int64_t to) {
+#pragma unroll
+            for (int n = 0; n < kRowLoads; ++n) {
+                const int b = first + 2 * n, c = b * 16 + lane;
+                if (c < vec) *reinterpret_cast<uint2*>(p.xq + to * p.H + c * 8) = codes[n];
+                if (lane == 0 && b < blocks) p.xs[to * ld + b] = static_cast<uint8_t>(byte[n]);
+            }
+        };
+        if (BY_TOKEN) {
+            for (int j = 0; j < p.k; ++j) {
+                const int64_t slot = token * p.k + j;
+                const int32_t at = p.inv[slot];
+                // a slot that the plan skipped has no entry: whatever is there
+                // does not lead back to it
+                if (at >= 0 && at < p.slots && p.perm[at] == slot) write(at);
+            }
+            if (p.S > 0) write(p.slots + token);
+        } else {
+            write(row);
+        }
+    }
+}
+
+// inv[perm[p]] = p.
+__global__ void __launch_bounds__(256) fp8_invert_kernel(const int32_t* perm, int32_t* inv,
+                                                         int64_t n) {
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; p < n;
+         p += static_cast<int64_t>(gridDim.x) * 256) {
+        const int32_t q = perm[p];
+        if (q >= 0 && q < n) inv[q] = static_cast<int32_t>(p);
     }
 }
 
@@ -192,14 +245,23 @@ cudaError_t launch_fp8_quantize_weights(const void* w, bool bf16, int64_t n, int
 
 cudaError_t launch_fp8_quantize_rows(const moe_shape& s, const Fp8Operands& o, int num_sms,
                                      cudaStream_t st) {
-    const int64_t slots = s.T * s.k, rows = slots + (s.n_shared > 0 ? s.T : 0);
-    const int64_t total = rows * ((s.H + kFp8Block - 1) / kFp8Block);
     const Fp8Tiles tiles = fp8_tiles(s);
-    int64_t grid = (total + 15) / 16;
-    if (grid > static_cast<int64_t>(num_sms) * 16) grid = static_cast<int64_t>(num_sms) * 16;
-    return launch_pdl(fp8_quantize_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st,
-                      static_cast<const uint4*>(o.x), o.perm, slots, rows, s.k, s.H, o.xq, o.xs, o.arrived,
-                      fp8_is_split(s) ? static_cast<int>(tiles.gate_up + tiles.down) : 0);
+    const bool by_token = fp8_by_token(s);
+    const QuantRowsParams p{static_cast<const uint4*>(o.x), o.perm, o.inv, s.T, s.T * s.k, s.k,
+                            s.n_shared, s.H, o.xq, o.xs, o.arrived,
+                            fp8_is_split(s) ? static_cast<int>(tiles.gate_up + tiles.down) : 0};
+    const int64_t most = static_cast<int64_t>(num_sms) * 8;
+    auto grid_for = [&](int64_t ctas) { return dim3(static_cast<unsigned>(ctas < most ? ctas : most)); };
+    if (by_token) {
+        const cudaError_t e = launch_pdl(fp8_invert_kernel, grid_for((p.slots + 255) / 256),
+                                         dim3(256), 0, st, o.perm, o.inv, p.slots);
+        if (e != cudaSuccess) return e;
+    }
+    const int blocks = (s.H + kFp8Block - 1) / kFp8Block;
+    const int64_t rows = by_token ? s.T : p.slots + (s.n_shared > 0 ? s.T : 0);
+    const int64_t warps = rows * ((blocks + kRowBlocks - 1) / kRowBlocks);
+    return launch_pdl(by_token ? fp8_quantize_rows_kernel<true> : fp8_quantize_rows_kernel<false>,
+                      grid_for((warps + 7) / 8), dim3(256), 0, st, p);
 }
 
 }  // namespace moe
