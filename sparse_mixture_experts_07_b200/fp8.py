@@ -106,6 +106,9 @@ def forward_fp8(shape: Shape, x, offsets, perm, topk_w, fp8: dict, workspace=Non
     check_fp8_experts(shape, fp8, dev)
     if y_slots is not None:
         _tensor("y_slots", y_slots, (shape.slot_rows, shape.H), shape.torch_dtype, dev)
+    for name, t in (("workspace", workspace), ("err_flag", err_flag)):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the tensors on {dev}")
     with _launch(dev, stream) as st:
         if workspace is None:
             workspace = alloc_fp8_workspace(shape, dev)

@@ -255,9 +255,11 @@ def _grad_arrays(grads):
         (ctypes.c_int32 * n)(*types)
 
 
-def _no_grads(dev):
+def _check_clip(dev, workspace=None):
     if dev is None:
         raise ValueError("no gradients given")
+    if workspace is not None and workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the gradients on {dev}")
 
 
 def grad_square_sum(grads: Sequence[Optional[torch.Tensor]], workspace=None, stream=None):
@@ -265,7 +267,7 @@ def grad_square_sum(grads: Sequence[Optional[torch.Tensor]], workspace=None, str
     different gradients sum it over their group before clip_grads."""
     lib = load_library()
     dev, n, ptrs, sizes, types = _grad_arrays(grads)
-    _no_grads(dev)
+    _check_clip(dev, workspace)
     with _launch(dev, stream) as s:
         ws = alloc_grad_norm_workspace(dev) if workspace is None else workspace
         total = torch.empty(1, dtype=torch.float64, device=dev)
@@ -279,7 +281,7 @@ def clip_grads(grads, max_norm: float, square_sum, stream=None):
     (float64 [1], from grad_square_sum); returns the norm, [1] float32."""
     lib = load_library()
     dev, n, ptrs, sizes, types = _grad_arrays(grads)
-    _no_grads(dev)
+    _check_clip(dev)
     _tensor("square_sum", square_sum, (1,), torch.float64, dev)
     with _launch(dev, stream) as s:
         norm_out = torch.empty(1, dtype=torch.float32, device=dev)
@@ -293,7 +295,7 @@ def clip_grad_norm(grads, max_norm: float, workspace=None, stream=None):
     norm before clipping, [1] float32 on the device (nothing synchronises)."""
     lib = load_library()
     dev, n, ptrs, sizes, types = _grad_arrays(grads)
-    _no_grads(dev)
+    _check_clip(dev, workspace)
     with _launch(dev, stream) as s:
         ws = alloc_grad_norm_workspace(dev) if workspace is None else workspace
         norm_out = torch.empty(1, dtype=torch.float32, device=dev)

@@ -749,3 +749,28 @@ def test_large_values_and_small_variance(cuda_ok):
     got = moe.norm_backward(_shape(T, H, dtype=torch.float32), moe.Norm("layer", 0.0), x, d)["x"]
     want = ref.norm_backward(_np(x), _np(d), "layer", 0.0)["x"]
     assert rel_l2(_np(got), want) < 1000 * 256 * U
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", [None, "channel"])
+def test_sublayer_without_a_norm_after(cuda_ok, gate):
+    """No norm after the block: the gate and the scale alone, forward and backward."""
+    inp, sub, h, (po, _, _), gt = _sublayer(SUB, gate, nxt=False)
+    sub.post = None
+    dh = torch.randn(SUB.T, SUB.H, generator=torch.Generator().manual_seed(10)).to(torch.bfloat16)
+    h2, saved = sub.forward_train(h.cuda())
+    got = sub.backward(saved, dh.cuda())
+    scale, y = np.float64(np.float32(0.22)), _np(saved["y"])
+    none = dict(kind="none")
+    assert rel_l2(_np(h2), ref.residual_norm(y, _np(h), none, gt, scale, None)[0]) < BF16_TOL
+    gp = ref.norm_backward(y, _np(dh), gate=gt, scale=scale, **none)
+    gb = oracle.moe_backward({**inp, "x": saved["xn"].cpu()}, SUB.k, gp["x"],
+                             routed_scale=SUB.routed_scale)
+    want = ref.norm_backward(_np(h), gb["x"], dadd=_np(dh), **po)
+    assert rel_l2(_np(got["h"]), want["x"]) < 2 * BF16_TOL
+    assert rel_l2(_np(got["pre_weight"]), want["weight"]) < 2 * BF16_TOL
+    assert "post_weight" not in got and ("gate" in got) == (gate is not None)
+    if gate:
+        assert rel_l2(_np(got["gate"]), gp["gate"]) < 1e-5
+    # serving gives the same h'
+    assert rel_l2(_np(sub(h.cuda())[0]), _np(h2)) < BF16_TOL
