@@ -123,7 +123,7 @@ struct Fp8Operands {
 // Batches whose K-blocks are shared out over the SMs rather than whole tiles:
 // few rows per expert, so that what takes the time is reading the weights, and
 // a tile's sums are small.
-inline bool fp8_is_split(const moe_shape& s) { return s.T <= 64; }
+inline bool fp8_is_split(const moe_shape& s) { return s.T <= 32; }
 // Batches whose activations are rounded once per token rather than once per
 // slot, through the inverse permutation.
 inline bool fp8_by_token(const moe_shape& s) { return !fp8_is_split(s) && s.k + s.n_shared > 1; }

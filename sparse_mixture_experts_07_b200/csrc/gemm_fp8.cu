@@ -27,10 +27,10 @@
 // as many reads.  The rest is the epilogue, 128 multiply-adds per thread and
 // K-block behind the tensor-memory loads.
 //
-// SPLIT (up to 64 tokens): reading the weights is what takes the time, and a
+// SPLIT (up to 32 tokens): reading the weights is what takes the time, and a
 // tile per CTA leaves SMs idle, so that K-blocks are shared out instead (see
-// Walk).  One token, two experts of 4096 x 6400: 50 us for 157 MB; 16 tokens
-// 164 us against 194 us for whole tiles.
+// Walk).  Experts of 4096 x 6400, top-2 of 16: one token 52 us for 157 MB, 16
+// tokens 171 us (whole tiles: 192), 32 tokens 201 (201), 64 tokens 235 (230).
 #include "fp8.cuh"
 #include "gemm_common.cuh"
 
@@ -161,10 +161,9 @@ __device__ __forceinline__ float row_weight(const GemmParams& p, const TileCoord
 }
 
 // The tiles a CTA computes, in the order that its producer, MMA and epilogue
-// warps all walk.  Without SPLIT: every workers-th tile, whole.  With SPLIT,
-// fewer tiles than CTAs: each tile in as many equal parts as there are CTAs
-// for; else the K-blocks of all tiles in a row, an equal share per CTA, which
-// may begin and end inside a tile.
+// warps all walk.  Without SPLIT: every workers-th tile, whole.  With SPLIT:
+// the K-blocks of all tiles in a row, an equal share per CTA, which may begin
+// and end inside a tile.
 struct Segment {
     TileCoord c;
     int tile, num_kb, kb0, kb1;     // K-blocks [kb0, kb1) of num_kb
@@ -176,8 +175,7 @@ template <int EPI, bool SPLIT> struct Walk {
     int worker, workers;
     int kb_routed, kb_shared;       // K-blocks of a tile
     int routed_tiles;
-    int parts;                      // SPLIT: per tile; 0: shares
-    int share, longer;              // K-blocks per CTA, one more in the first `longer`
+    int share, longer;              // SPLIT: K-blocks per CTA, one more in the first `longer`
     int pos, end;                   // SPLIT: K-blocks; else tiles
     __device__ __forceinline__ Walk(const GroupTable& gt, const GemmParams& p)
         : gt(gt), p(p), worker(blockIdx.x), workers(gridDim.x) {
@@ -185,13 +183,11 @@ template <int EPI, bool SPLIT> struct Walk {
         kb_shared = (p.K_shared + fp8g::BK - 1) / fp8g::BK;
         routed_tiles = gt.tile_start[p.E];
         if (SPLIT) {
-            const int tiles = gt.total_tiles, blocks = first_block(tiles);
-            parts = tiles == 0 || tiles > workers ? 0 : workers / tiles;
+            const int blocks = first_block(gt.total_tiles);
             share = blocks / workers;
             longer = blocks - share * workers;
-            const bool idle = parts > 0 && worker >= tiles * parts;
-            pos = idle ? 0 : begin_of(worker);
-            end = idle ? 0 : begin_of(worker + 1);
+            pos = begin_of(worker);
+            end = begin_of(worker + 1);
         } else {
             pos = worker;
             end = gt.total_tiles;
@@ -202,24 +198,8 @@ template <int EPI, bool SPLIT> struct Walk {
         return min(tile, routed_tiles) * kb_routed + max(tile - routed_tiles, 0) * kb_shared;
     }
     // first K-block of CTA w
-    __device__ __forceinline__ int begin_of(int w) const {
-        if (parts > 0) {
-            const int tile = w / parts;
-            return first_block(tile) +
-                   (w - tile * parts) * (tile < routed_tiles ? kb_routed : kb_shared) / parts;
-        }
-        return w * share + min(w, longer);
-    }
-    // CTAs that compute parts of a tile
-    __device__ __forceinline__ void workers_of(const Segment& s, int& w0, int& w1) const {
-        if (parts > 0) {
-            w0 = s.tile * parts;
-            w1 = w0 + parts - 1;
-        } else {
-            w0 = worker_of(first_block(s.tile));
-            w1 = worker_of(first_block(s.tile) + s.num_kb - 1);
-        }
-    }
+    __device__ __forceinline__ int begin_of(int w) const { return w * share + min(w, longer); }
+    // CTA that computes K-block b
     __device__ __forceinline__ int worker_of(int b) const {
         const int in_longer = longer * (share + 1);
         return b < in_longer ? b / (share + 1) : longer + (b - in_longer) / share;
@@ -314,8 +294,7 @@ __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const
     const int lane = threadIdx.x & 31;
     const int N = c.routed ? p.N_routed : p.N_shared;
     const int first = walk.first_block(sg.tile);
-    int w0, w1;
-    walk.workers_of(sg, w0, w1);
+    const int w0 = walk.worker_of(first), w1 = walk.worker_of(first + sg.num_kb - 1);
     const int rows = min(c.rows - c.m0, fp8g::BM);
     // this lane's columns of the tile: 4 of gate and of up, or twice 4 of y
     const int ca = 4 * lane, cb = 128 + 4 * lane;
@@ -329,7 +308,6 @@ __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const
                 va[i] = vb[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (w + i > w1) continue;
                 const int begin = walk.begin_of(w + i);
-                if (walk.begin_of(w + i + 1) == begin) continue;    // more parts than K-blocks
                 const float* from = fp.part + ((static_cast<int64_t>(w + i) * 2 +
                                                 (begin <= first)) * fp.part_rows + r) * fp8g::BN;
                 va[i] = __ldcg(reinterpret_cast<const float4*>(from + ca));

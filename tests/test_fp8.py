@@ -360,9 +360,9 @@ def test_layer_graph_stream_and_sublayer(cuda_ok, T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 2, 16, 63, 64, 65, 128])
+@pytest.mark.parametrize("T", [1, 2, 16, 31, 32, 33, 64, 128])
 def test_batch_sizes_around_the_split(cuda_ok, T):
-    """Up to 64 tokens share K-blocks out over the SMs, tiles then being summed
+    """Up to 32 tokens share K-blocks out over the SMs, tiles then being summed
     from parts; a tile may also lie whole in one share."""
     for H, I, E, k, S, Is in ((1280, 640, 6, 2, 1, 384), (256, 4096, 64, 6, 0, 0)):
         args = _setup(T, H, I, E, k, S, Is, seed=T)
@@ -372,7 +372,7 @@ def test_batch_sizes_around_the_split(cuda_ok, T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [8, 64, 300])
+@pytest.mark.parametrize("T", [8, 32, 64, 300])
 def test_every_slot_on_one_expert(cuda_ok, T):
     """A plan may name one expert in all of a token's slots: more rows in a
     group than tokens."""
