@@ -123,14 +123,15 @@ struct Fp8Operands {
 // Batches whose K-blocks are shared out over the SMs rather than whole tiles:
 // few rows per expert, so that what takes the time is reading the weights, and
 // a tile's sums are small.
-inline bool fp8_is_split(const moe_shape& s) { return s.T <= 32; }
+constexpr int kFp8SplitRows = 32;      // rows of their tiles
+inline bool fp8_is_split(const moe_shape& s) { return s.T <= kFp8SplitRows; }
 // Batches whose activations are rounded once per token rather than once per
 // slot, through the inverse permutation.
 inline bool fp8_by_token(const moe_shape& s) { return !fp8_is_split(s) && s.k + s.n_shared > 1; }
 
-// Rows of one tile of such a batch (a plan may give an expert every slot).
+// Most rows of one such tile with data.
 inline int fp8_part_rows(const moe_shape& s) {
-    return static_cast<int>(s.T * s.k < 128 ? s.T * s.k : 128);
+    return static_cast<int>(s.T * s.k < kFp8SplitRows ? s.T * s.k : kFp8SplitRows);
 }
 
 // At most this many tiles: every group may end in a partial m-tile.
@@ -139,8 +140,9 @@ struct Fp8Tiles {
 };
 inline Fp8Tiles fp8_tiles(const moe_shape& s) {
     const int64_t slots = s.T * s.k;
-    const int64_t m = (slots + 127) / 128 + (s.E < slots ? s.E : slots);
-    const int64_t ms = s.n_shared * ((s.T + 127) / 128);
+    const int64_t rows = fp8_is_split(s) ? kFp8SplitRows : 128;
+    const int64_t m = (slots + rows - 1) / rows + (s.E < slots ? s.E : slots);
+    const int64_t ms = s.n_shared * ((s.T + rows - 1) / rows);
     const int64_t Is = s.n_shared > 0 ? s.I_shared : 0;
     return {m * ((s.I + 127) / 128) + ms * ((Is + 127) / 128), (m + ms) * ((s.H + 255) / 256)};
 }

@@ -37,11 +37,11 @@
 namespace moe {
 
 namespace fp8g {
-constexpr int BM = 128;                    // rows per CTA
+constexpr int BM = 128;                    // MMA rows
 constexpr int BN = 256;
 constexpr int BK = 128;                    // codes (bytes) per K-block
 constexpr int UMMA_K = 32;
-constexpr int TILE_BYTES = 128 * BK;       // 128 rows of A or of B: 16 KB
+constexpr int TILE_BYTES = 128 * BK;       // 128 rows of B: 16 KB
 constexpr int TMEM_COLS = 512;
 constexpr int EPI_WARPS = 8;
 // One warpgroup for the producer and MMA warps (two of its warps idle), two for
@@ -49,9 +49,16 @@ constexpr int EPI_WARPS = 8;
 // not need: 128 x 56 + 256 x 224 = 384 x 168, what the block is launched with.
 constexpr int THREADS = 128 + EPI_WARPS * 32;
 constexpr int REGS_FEW = 56, REGS_MANY = 224;
-constexpr int STAGE_BYTES = 3 * TILE_BYTES;   // 128 rows of A, 2 x 128 of B
-constexpr int STAGES = 4;                     // 192 KB
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
+// Rows of a tile that hold data.  With SPLIT (few rows per expert) 32 of the
+// MMA's 128: the others read what follows the A rows in the stage, and what
+// they compute is not looked at.  A stage is then 36 KB, and six of them fit.
+template <bool SPLIT> struct Cfg {
+    static constexpr int ROWS = SPLIT ? kFp8SplitRows : BM;
+    static constexpr int A_BYTES = ROWS * BK;
+    static constexpr int STAGE_BYTES = A_BYTES + 2 * TILE_BYTES;   // A, 2 x 128 rows of B
+    static constexpr int STAGES = SPLIT ? 6 : 4;                   // 216, 192 KB
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 256;
+};
 }  // namespace fp8g
 
 struct Fp8GemmParams {
@@ -224,12 +231,13 @@ template <int EPI, bool SPLIT> struct Walk {
         return true;
     }
     __device__ __forceinline__ TileCoord tile_coord(int tile) const {
-        return decode_tile(gt, p, tile, EPI == kSwiGLU ? fp8g::BN / 2 : fp8g::BN, fp8g::BM);
+        return decode_tile(gt, p, tile, EPI == kSwiGLU ? fp8g::BN / 2 : fp8g::BN,
+                           fp8g::Cfg<SPLIT>::ROWS);
     }
 };
 
 // The group table, by one warp, 32 groups at a time.
-__device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p) {
+__device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p, int tile_rows) {
     const int lane = threadIdx.x & 31;
     int start = 0;
     for (int g0 = 0; g0 < p.E + p.S; g0 += 32) {
@@ -244,7 +252,7 @@ __device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p)
             row0 = static_cast<int>((g - p.E) * p.T);
             rows = static_cast<int>(p.T);
         }
-        const int tiles = (rows + fp8g::BM - 1) / fp8g::BM *
+        const int tiles = (rows + tile_rows - 1) / tile_rows *
                           (g < p.E ? p.n_tiles_routed : p.n_tiles_shared);
         int sum = tiles;
 #pragma unroll
@@ -295,7 +303,7 @@ __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const
     const int N = c.routed ? p.N_routed : p.N_shared;
     const int first = walk.first_block(sg.tile);
     const int w0 = walk.worker_of(first), w1 = walk.worker_of(first + sg.num_kb - 1);
-    const int rows = min(c.rows - c.m0, fp8g::BM);
+    const int rows = min(c.rows - c.m0, fp8g::Cfg<SPLIT>::ROWS);
     // this lane's columns of the tile: 4 of gate and of up, or twice 4 of y
     const int ca = 4 * lane, cb = 128 + 4 * lane;
     for (int r = warp; r < rows; r += fp8g::EPI_WARPS) {
@@ -361,11 +369,14 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     const __grid_constant__ CUtensorMap map_b_routed,
     const __grid_constant__ CUtensorMap map_b_shared, const Fp8GemmParams fp) {
     using namespace fp8g;
+    using C = Cfg<SPLIT>;
+    constexpr int ROWS = C::ROWS, A_BYTES = C::A_BYTES, STAGE_BYTES = C::STAGE_BYTES,
+                  STAGES = C::STAGES;
     const GemmParams& p = fp.g;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ GroupTable gt;
     __shared__ uint32_t tmem_base_sh;
-    __shared__ int last_sh;
+    __shared__ bool last_sh[2];                 // SPLIT: this CTA completes the tile
     __shared__ uint32_t mag_sh[2][2][BM];       // [tile parity][column half][row]
 
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     // pdl_wait: what the kernels before the previous one wrote (the plan) and
     // the weights are there already, so the table is built and the first weight
     // tiles are loaded while the previous kernel still runs.
-    if (warp == 0) build_table(gt, p);
+    if (warp == 0) build_table(gt, p, ROWS);
     if (threadIdx.x == 32) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -433,7 +444,7 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                         const TileSource src = tile_source<EPI>(p, gt, sg.c);
                         const CUtensorMap* mb = sg.c.routed ? &map_b_routed : &map_b_shared;
                         for (int kb = sg.kb0; kb < sg.kb1 && ahead < STAGES; ++kb, ++ahead) {
-                            uint8_t* sb = smem + ahead * STAGE_BYTES + TILE_BYTES;
+                            uint8_t* sb = smem + ahead * STAGE_BYTES + A_BYTES;
                             mbar_arrive_expect_tx(&full[ahead], STAGE_BYTES);
                             tma_load_2d(sb, mb, &full[ahead], kb * BK, src.b_row);
                             tma_load_2d(sb + TILE_BYTES, mb, &full[ahead], kb * BK, src.b_row2);
@@ -457,8 +468,8 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                                 break;
                             }
                             mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
-                            tma_load_2d(sa + TILE_BYTES, mb, &full[stage], kb * BK, src.b_row);
-                            tma_load_2d(sa + 2 * TILE_BYTES, mb, &full[stage], kb * BK,
+                            tma_load_2d(sa + A_BYTES, mb, &full[stage], kb * BK, src.b_row);
+                            tma_load_2d(sa + A_BYTES + TILE_BYTES, mb, &full[stage], kb * BK,
                                         src.b_row2);
                         }
                         tma_load_2d(sa, ma, &full[stage], kb * BK, src.a_row);
@@ -492,7 +503,7 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                         tc_fence_after();
                         const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
                         const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-                        const uint32_t sb = sa + TILE_BYTES;
+                        const uint32_t sb = sa + A_BYTES;
 #pragma unroll
                         for (int kk = 0; kk < BK / UMMA_K; ++kk)
                             umma_e4m3(d, smem_desc_sw128(sa + kk * UMMA_K),
@@ -526,14 +537,18 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
         // after a wait that ran out, the loops still run to their end (the
         // epilogue barrier needs every warp) without waiting or storing
         bool ok = true;
+        // tiles that this CTA has left a part of: one begun by another CTA, one
+        // that another goes on with
+        int pending[2] = {-1, -1};
         while (walk.next(sg)) {
             const TileCoord& c = sg.c;
             const int N = c.routed ? p.N_routed : p.N_shared;
             const int num_kb = sg.num_kb;
             const int eidx = c.routed ? c.g : c.g - p.E;
             const int m = c.m0 + row;
-            const bool valid = m < c.rows;
-            const bool any = m - lane < c.rows;      // of this warp's rows
+            const bool valid = row < ROWS && m < c.rows;
+            // of this warp's rows
+            const bool any = quarter * 32 < ROWS && m - lane < c.rows;
             const int64_t a_row =
                 (EPI == kSwiGLU && !c.routed ? 0 : static_cast<int64_t>(gt.row0[c.g])) +
                 (valid ? m : c.rows - 1);
@@ -604,8 +619,7 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                 if (++buf == 2) { buf = 0; buf_phase ^= 1u; }
             }
             if (SPLIT && sg.kb1 - sg.kb0 < num_kb) {
-                // a part of the tile: leave its sums (in the tile's columns), and
-                // finish the tile if all parts are now there
+                // a part of the tile: leave its sums, in the tile's columns
                 float* mine = fp.part + ((static_cast<int64_t>(walk.worker) * 2 + (sg.kb0 == 0)) *
                                              fp.part_rows + row) * BN;
                 if (valid) {
@@ -617,15 +631,7 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                             acc[64 + j], acc[64 + j + 1], acc[64 + j + 2], acc[64 + j + 3]);
                     }
                 }
-                __threadfence();
-                epilogue_sync();
-                if (threadIdx.x == 128) {
-                    const int n = sg.kb1 - sg.kb0;
-                    last_sh = atomicAdd(fp.arrived + sg.tile, n) + n == num_kb;
-                    __threadfence();
-                }
-                epilogue_sync();
-                if (last_sh && ok) finish_parts<EPI, SPLIT>(walk, sg, gt, fp, warp - 4);
+                pending[sg.kb0 == 0] = sg.tile;
                 continue;
             }
             if (EPI == kSwiGLU) {
@@ -699,6 +705,33 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                 }
             }
         }
+        if (SPLIT) {
+            // count the parts in, once for both tiles; whoever completes a tile
+            // finishes it
+            __threadfence();
+            epilogue_sync();
+            if (threadIdx.x == 128) {
+                for (int i = 0; i < 2; ++i) {
+                    last_sh[i] = false;
+                    if (pending[i] < 0) continue;
+                    const int first = walk.first_block(pending[i]);
+                    const int blocks = pending[i] < walk.routed_tiles ? walk.kb_routed
+                                                                      : walk.kb_shared;
+                    const int n = min(first + blocks, walk.end) -
+                                  max(first, walk.begin_of(walk.worker));
+                    last_sh[i] = atomicAdd(fp.arrived + pending[i], n) + n == blocks;
+                }
+                __threadfence();
+            }
+            epilogue_sync();
+            for (int i = 0; i < 2; ++i) {
+                if (!last_sh[i] || !ok) continue;
+                sg.tile = pending[i];
+                sg.c = walk.tile_coord(sg.tile);
+                sg.num_kb = sg.c.routed ? walk.kb_routed : walk.kb_shared;
+                finish_parts<EPI, SPLIT>(walk, sg, gt, fp, warp - 4);
+            }
+        }
     }
 
     tc_fence_before();
@@ -711,13 +744,14 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
 
 namespace {
 
-// Codes [rows, cols], box of 128 columns x 128 rows, 128-byte swizzle.
-bool make_map_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t cols) {
+// Codes [rows, cols], box of 128 columns x box_rows rows, 128-byte swizzle.
+bool make_map_codes(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
+                    int box_rows = 128) {
     EncodeTiledFn enc = get_encode_fn();
     if (!enc || rows <= 0 || cols <= 0) return false;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-    cuuint32_t box[2] = {fp8g::BK, 128u};
+    cuuint32_t box[2] = {fp8g::BK, static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -732,7 +766,7 @@ cudaError_t launch_gemm(const Fp8GemmParams& p, int64_t tiles, int num_sms,
     using namespace fp8g;
     auto kern = grouped_gemm_fp8<EPI, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SMEM_BYTES);
+                                         Cfg<SPLIT>::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     // the register split assumes what the block is launched with
     static const bool split_fits = [&] {
@@ -742,7 +776,8 @@ cudaError_t launch_gemm(const Fp8GemmParams& p, int64_t tiles, int num_sms,
     }();
     if (!split_fits) return cudaErrorLaunchOutOfResources;
     const int64_t grid = SPLIT || tiles > num_sms ? num_sms : tiles;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(THREADS), SMEM_BYTES, st, ar,
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(THREADS),
+                      Cfg<SPLIT>::SMEM_BYTES, st, ar,
                       as, br, bs, p);
 }
 
@@ -754,14 +789,16 @@ cudaError_t launch_ffn_fp8(const moe_shape& s, const Fp8Operands& o, int num_sms
     const int64_t Tk = s.T * s.k;
     const int S = s.n_shared, Is = S > 0 ? s.I_shared : s.I;
     CUtensorMap a1r, a1s, b1r, b1s, a2r, a2s, b2r, b2s;
-    bool ok = make_map_codes(&a1r, o.xq, Tk, s.H);
+    const bool split = fp8_is_split(s);
+    const int a_rows = split ? kFp8SplitRows : fp8g::BM;
+    bool ok = make_map_codes(&a1r, o.xq, Tk, s.H, a_rows);
     ok &= make_map_codes(&b1r, o.gate_up, static_cast<int64_t>(s.E) * 2 * s.I, s.H);
-    ok &= make_map_codes(&a2r, o.hq, Tk, s.I);
+    ok &= make_map_codes(&a2r, o.hq, Tk, s.I, a_rows);
     ok &= make_map_codes(&b2r, o.down, static_cast<int64_t>(s.E) * s.H, s.I);
     if (S > 0) {
-        ok &= make_map_codes(&a1s, o.xq + Tk * s.H, s.T, s.H);
+        ok &= make_map_codes(&a1s, o.xq + Tk * s.H, s.T, s.H, a_rows);
         ok &= make_map_codes(&b1s, o.sh_gate_up, static_cast<int64_t>(S) * 2 * Is, s.H);
-        ok &= make_map_codes(&a2s, o.hq_sh, S * s.T, Is);
+        ok &= make_map_codes(&a2s, o.hq_sh, S * s.T, Is, a_rows);
         ok &= make_map_codes(&b2s, o.sh_down, static_cast<int64_t>(S) * s.H, Is);
     } else {
         a1s = a1r; b1s = b1r; a2s = a2r; b2s = b2r;
@@ -801,7 +838,6 @@ cudaError_t launch_ffn_fp8(const moe_shape& s, const Fp8Operands& o, int num_sms
     p.hs_routed = o.hs;
     p.hs_shared = o.hs_sh;
     const Fp8Tiles tiles = fp8_tiles(s);
-    const bool split = fp8_is_split(s);
     p.part = o.part;
     p.part_rows = fp8_part_rows(s);
     p.arrived = o.arrived;
