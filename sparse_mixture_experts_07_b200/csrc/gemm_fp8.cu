@@ -29,8 +29,10 @@
 //
 // SPLIT (up to 32 tokens): reading the weights is what takes the time, and a
 // tile per CTA leaves SMs idle, so that K-blocks are shared out instead (see
-// Walk).  Experts of 4096 x 6400, top-2 of 16: one token 52 us for 157 MB, 16
-// tokens 171 us (whole tiles: 192), 32 tokens 201 (201), 64 tokens 235 (230).
+// Walk).  Experts of 4096 x 6400, top-2 of 16: one token 46 us for 157 MB, 8
+// tokens 130 us, 16 tokens 168 us (whole tiles 192), 32 tokens 197 us (201); at
+// 64 tokens whole tiles are no slower (230 against 232), at 128 faster (233
+// against 271).
 #include "fp8.cuh"
 #include "gemm_common.cuh"
 
