@@ -446,3 +446,17 @@ def test_offsets_past_32_bits(cuda_ok):
             want *= w[rows, e].double().cpu().numpy()[:, None]
             got = y[e * T + t0:e * T + t0 + 40].double().cpu().numpy()
             assert rel_l2(got, want) <= TOL + 2.0 ** -3 / np.sqrt(40 * I)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 90, 400])
+def test_outputs_off_the_32_byte_boundary(cuda_ok, T):
+    """y_slots and the workspace may start on any 16-byte boundary."""
+    for I in (272, 288):
+        shape, x, perm, offsets, w, fp8 = _setup(T, 144, I, 4, 2, 1, 96, seed=9)
+        want = _run(shape, x, perm, offsets, w, fp8)
+        y = torch.zeros(shape.slot_rows * shape.H + 8, dtype=torch.bfloat16, device="cuda")[8:]
+        ws = torch.zeros(moe.fp8_workspace_size(shape) + 16, dtype=torch.uint8, device="cuda")[16:]
+        got = _run(shape, x, perm, offsets, w, fp8, y_slots=y.view(shape.slot_rows, shape.H),
+                   workspace=ws)
+        assert got.data_ptr() % 32 == 16 and torch.equal(got, want)
