@@ -22,7 +22,7 @@
 // per K-block, and the Mixtral-shaped layer took 3.87 ms against 2.15 ms.
 //
 // Bounds, measured on a B200: 4096 tokens, 8 experts of 4096 x 14336 take
-// 1.74 ms (1.66 PFLOP/s; 2.0 ms at the power cap).  Without the epilogue's work
+// 1.71 ms (1.69 PFLOP/s; 2.0 ms at the power cap).  Without the epilogue's work
 // 1.34 ms: a K-block's operands cost one SM 48 KB of shared-memory writes and
 // as many reads.  The rest is the epilogue, 128 multiply-adds per thread and
 // K-block behind the tensor-memory loads.
@@ -154,7 +154,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // 32 bytes of a row.  A thread writes its own row, so that a warp's store
 // touches 32 rows: 32-byte stores fill whole sectors (16384 tokens, 64 experts
-// of 2048 x 1024: 1165 us against 1235 us in pairs of 16 bytes).
+// of 2048 x 1024: 1153 us against 1235 us in pairs of 16 bytes).
 __device__ __forceinline__ void store32(void* p, const uint32_t (&o)[8], bool wide) {
     if (wide) {
         asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(o[0]),
@@ -253,7 +253,8 @@ template <int EPI, bool SPLIT> struct Walk {
     }
 };
 
-// The group table, by one warp, 32 groups at a time.
+// The group table, by one warp, 32 groups at a time.  It is read before
+// pdl_wait, hence from L2: a line of an earlier plan may still be in L1.
 __device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p, int tile_rows) {
     const int lane = threadIdx.x & 31;
     int start = 0;
@@ -263,8 +264,8 @@ __device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p,
         if (g < p.E) {
             // kept inside the slots, whatever the offsets say
             const int slots = static_cast<int>(p.T * p.k);
-            row0 = min(max(p.offsets[g], 0), slots);
-            rows = max(min(p.offsets[g + 1], slots) - row0, 0);
+            row0 = min(max(__ldcg(p.offsets + g), 0), slots);
+            rows = max(min(__ldcg(p.offsets + g + 1), slots) - row0, 0);
         } else if (g < p.E + p.S) {
             row0 = static_cast<int>((g - p.E) * p.T);
             rows = static_cast<int>(p.T);

@@ -460,3 +460,34 @@ def test_outputs_off_the_32_byte_boundary(cuda_ok, T):
         got = _run(shape, x, perm, offsets, w, fp8, y_slots=y.view(shape.slot_rows, shape.H),
                    workspace=ws)
         assert got.data_ptr() % 32 == 16 and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 7, 32, 200, 700])
+def test_replays_follow_the_routing(cuda_ok, T):
+    """A captured step whose tokens, and with them the plan, change from replay
+    to replay, and eager steps back to back: as a fresh layer computes each."""
+    H, I, E, k = 256, 272, 8, 2
+    g = torch.Generator().manual_seed(12)
+    fp8 = moe.fp8_experts((torch.randn(E, 2 * I, H, generator=g) * 0.05).cuda(),
+                          (torch.randn(E, H, I, generator=g) * 0.05).cuda())
+    wr = torch.randn(E, H, generator=g).cuda()
+    shape = moe.Shape(T=T, H=H, I=I, E=E, k=k)
+    xs = [torch.randn(T, H, generator=g).to(torch.bfloat16).cuda() for _ in range(6)]
+    want = []
+    for x in xs:
+        fresh = moe.MoELayer(shape, wr, None, fp8=fp8)
+        torch.cuda.synchronize()
+        want.append(fresh(x).clone())
+        torch.cuda.synchronize()
+    layer = moe.MoELayer(shape, wr, None, fp8=fp8)
+    got = [layer(x, y=torch.empty_like(x)) for x in xs]          # nothing waits between
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    static = xs[0].clone()
+    graph = layer.capture(static)
+    for _ in range(3):
+        for x, w in zip(xs, want):
+            static.copy_(x)
+            assert torch.equal(graph.replay(), w)
+    assert layer.device_error() == 0
