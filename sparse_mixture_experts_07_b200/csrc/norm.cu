@@ -498,11 +498,15 @@ __global__ void __launch_bounds__(1024) norm_params_kernel(const NormBackwardPar
     }
 }
 
-// CTAs of `kern` that are resident at once on the current device.
-template <typename K> int resident_ctas(K kern, int threads, int num_sms) {
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess ||
-        per_sm <= 0)
+// CTAs of `kern` that are resident at once on the current device (looked up
+// once per device and block size).
+template <typename K> int resident_ctas(K kern, int threads, int num_sms, int (&cache)[64][33]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    int& per_sm = cache[dev][threads / 32];
+    if (per_sm <= 0 &&
+        (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0) != cudaSuccess ||
+         per_sm <= 0))
         per_sm = 1;
     return num_sms * per_sm;
 }
@@ -513,7 +517,8 @@ template <typename T, int VEC, int VPT, int MAXT>
 cudaError_t run_combine_norm(const CombineNormParams& p, int num_sms, cudaStream_t st) {
     const int threads = threads_for(p.H / VEC, VPT);
     auto kern = combine_norm_kernel<T, VEC, VPT, MAXT>;
-    const int64_t cap = p.T <= num_sms ? num_sms : resident_ctas(kern, threads, num_sms);
+    static int resident[64][33] = {};
+    const int64_t cap = p.T <= num_sms ? num_sms : resident_ctas(kern, threads, num_sms, resident);
     return launch_pdl(kern, dim3(static_cast<unsigned>(p.T < cap ? p.T : cap)), dim3(threads), 0,
                       st, p);
 }

@@ -15,8 +15,8 @@ from typing import Optional
 
 import torch
 
-from .moe import MOE_BF16, MOE_F32, Shape, _check, _ptr, load_library
-from .sublayer import _cuda, _launch, _tensor
+from .moe import MOE_BF16, MOE_F32, Shape, _check, load_library
+from .sublayer import _addr, _cuda, _launch, _tensor
 
 CODE_TYPES = (torch.float8_e4m3fn, torch.uint8)
 
@@ -114,11 +114,11 @@ def forward_fp8(shape: Shape, x, offsets, perm, topk_w, fp8: dict, workspace=Non
             workspace = alloc_fp8_workspace(shape, dev)
         if y_slots is None:
             y_slots = torch.empty(shape.slot_rows, shape.H, dtype=shape.torch_dtype, device=dev)
-        sh = [_ptr(fp8.get(f"sh_{k}") if shape.n_shared else None)
+        sh = [_addr(fp8.get(f"sh_{k}") if shape.n_shared else None)
               for k in ("gate_up_q", "gate_up_s", "down_q", "down_s")]
         _check(lib.moe_forward_fp8(
             ctypes.byref(shape.c()), x.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
             topk_w.data_ptr(), fp8["gate_up_q"].data_ptr(), fp8["gate_up_s"].data_ptr(),
             fp8["down_q"].data_ptr(), fp8["down_s"].data_ptr(), *sh, y_slots.data_ptr(),
-            _ptr(err_flag), workspace.data_ptr(), workspace.numel(), st), "moe_forward_fp8")
+            _addr(err_flag), workspace.data_ptr(), workspace.numel(), st), "moe_forward_fp8")
     return y_slots

@@ -139,8 +139,13 @@ class Shape:
                      cfg.routed_scale, MOE_BF16 if cfg.dtype == "bf16" else MOE_F32)
 
     def c(self) -> MoEShape:
-        return MoEShape(self.T, self.H, self.I, self.E, self.k, self.n_shared, self.I_shared,
-                        self.routed_scale, self.dtype)
+        """The C struct, made once (a Shape does not change)."""
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = MoEShape(self.T, self.H, self.I, self.E, self.k, self.n_shared, self.I_shared,
+                         self.routed_scale, self.dtype)
+            object.__setattr__(self, "_c", c)
+        return c
 
     @property
     def torch_dtype(self):

@@ -16,7 +16,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import moe as _moe
-from .moe import MOE_BF16, MOE_F32, MoELayer, Shape, _check, _ptr, load_library
+from .moe import MOE_BF16, MOE_F32, MoELayer, Shape, _check, load_library
 
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
 GATE_NONE, GATE_TOKEN, GATE_CHANNEL = 0, 1, 2
@@ -57,9 +57,13 @@ def _tensor(name, t, size, dtype, device):
 
 
 def _cuda(t):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"expected CUDA tensors, got one on {t.device}")
     return t.device
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check_norm(name, n: Norm, H, device):
@@ -163,7 +167,7 @@ def combine_norm(shape: Shape, y_slots, inv, residual=None, post: Optional[Norm]
     with _launch(dev, stream) as s:
         h, xn, y = bufs.get("h"), None, None
         if h is None:
-            h = y_slots.new_empty(size)
+            h = y_slots.new_empty(size) if residual is None else torch.empty_like(residual)
         if next_norm is not None:
             xn = bufs.get("xn")
             if xn is None:
@@ -173,10 +177,10 @@ def combine_norm(shape: Shape, y_slots, inv, residual=None, post: Optional[Norm]
             if y is None:
                 y = torch.empty_like(h)
         _check(lib.moe_combine_norm(
-            ctypes.byref(shape.c()), y_slots.data_ptr(), inv.data_ptr(), _ptr(residual),
-            None if post is None else ctypes.byref(post.c()), kind, _ptr(gate), scale,
-            None if next_norm is None else ctypes.byref(next_norm.c()), _ptr(y), h.data_ptr(),
-            _ptr(xn), s), "moe_combine_norm")
+            ctypes.byref(shape.c()), y_slots.data_ptr(), inv.data_ptr(), _addr(residual),
+            None if post is None else ctypes.byref(post.c()), kind, _addr(gate), scale,
+            None if next_norm is None else ctypes.byref(next_norm.c()), _addr(y), h.data_ptr(),
+            _addr(xn), s), "moe_combine_norm")
     return h, xn, y
 
 
@@ -215,8 +219,8 @@ def norm_backward(shape: Shape, spec: Norm, x, dout, gate=None, scale: float = 1
              "gate": None if gate is None else torch.empty_like(gate)}
         _check(lib.moe_norm_backward(
             ctypes.byref(shape.c()), ctypes.byref(spec.c()), x.data_ptr(), dout.data_ptr(), kind,
-            _ptr(gate), scale, _ptr(dadd), g["x"].data_ptr(), _ptr(g["weight"]), _ptr(g["bias"]),
-            _ptr(g["gate"]), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _addr(gate), scale, _addr(dadd), g["x"].data_ptr(), _addr(g["weight"]), _addr(g["bias"]),
+            _addr(g["gate"]), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
             s), "moe_norm_backward")
     return g
 
@@ -229,30 +233,29 @@ def alloc_grad_norm_workspace(device="cuda") -> torch.Tensor:
     return torch.empty(n.value, dtype=torch.uint8, device=device)
 
 
+_GRAD_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
 def _grad_arrays(grads):
     """(device, n, pointers, sizes, types) of a list of dense gradients; None entries skipped."""
-    ptrs, sizes, types, dev = [], [], [], None
-    for g in grads:
-        if g is None:
-            continue
-        if g.dtype is torch.float32:
-            types.append(MOE_F32)
-        elif g.dtype is torch.bfloat16:
-            types.append(MOE_BF16)
-        else:
+    grads = [g for g in grads if g is not None]
+    n = len(grads)
+    dev = grads[0].device if n else None
+    types = (ctypes.c_int32 * n)()
+    for i, g in enumerate(grads):
+        kind = _GRAD_TYPES.get(g.dtype)
+        if kind is None:
             raise ValueError(f"gradients must be float32 or bfloat16, got {g.dtype}")
-        if dev is None:
-            dev = _cuda(g)
-        elif g.device != dev:
+        if g.device != dev:
             raise ValueError(f"gradients on {dev} and {g.device}: clip each device's alone, on "
                              "the all-reduced grad_square_sum")
         if not g.is_contiguous():
             raise ValueError(f"gradients must be contiguous, got strides {g.stride()}")
-        ptrs.append(g.data_ptr())
-        sizes.append(g.numel())
-    n = len(ptrs)
-    return dev, n, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*sizes), \
-        (ctypes.c_int32 * n)(*types)
+        types[i] = kind
+    if n:
+        _cuda(grads[0])
+    return dev, n, (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads]), \
+        (ctypes.c_int64 * n)(*[g.numel() for g in grads]), types
 
 
 def _check_clip(dev, workspace=None):
