@@ -29,8 +29,8 @@
 //
 // SPLIT (up to 32 tokens): reading the weights is what takes the time, and a
 // tile per CTA leaves SMs idle, so that K-blocks are shared out instead (see
-// Walk).  Experts of 4096 x 6400, top-2 of 16: one token 46 us for 157 MB, 8
-// tokens 130 us, 16 tokens 168 us (whole tiles 192), 32 tokens 197 us (201); at
+// Walk).  Experts of 4096 x 6400, top-2 of 16: one token 42 us for 157 MB, 8
+// tokens 127 us, 16 tokens 165 us (whole tiles 192), 32 tokens 193 us (201); at
 // 64 tokens whole tiles are no slower (230 against 232), at 128 faster (233
 // against 271).
 #include "fp8.cuh"
@@ -310,11 +310,12 @@ __device__ __forceinline__ TileSource tile_source(const GemmParams& p, const Gro
 }
 
 // Adds up the parts of a tile in the order of their K-blocks (whichever CTA
-// does it, the sum is the same) and writes the tile's rows, a warp per row.
+// does it, the sum is the same) and writes the tile's rows, a warp per row:
+// rows warp, warp + warps, ...
 template <int EPI, bool SPLIT>
 __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const Segment& sg,
                                              const GroupTable& gt, const Fp8GemmParams& fp,
-                                             int warp) {
+                                             int warp, int warps) {
     const GemmParams& p = fp.g;
     const TileCoord& c = sg.c;
     const int lane = threadIdx.x & 31;
@@ -324,13 +325,15 @@ __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const
     const int rows = min(c.rows - c.m0, fp8g::Cfg<SPLIT>::ROWS);
     // this lane's columns of the tile: 4 of gate and of up, or twice 4 of y
     const int ca = 4 * lane, cb = 128 + 4 * lane;
-    for (int r = warp; r < rows; r += fp8g::EPI_WARPS) {
+    for (int r = warp; r < rows; r += warps) {
+        const int64_t orow = static_cast<int64_t>(gt.row0[c.g]) + c.m0 + r;
+        const float weight = EPI == kScaled ? row_weight(p, c, orow) : 1.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        for (int w = w0; w <= w1; w += 4) {
-            // four workers' parts in flight, added in order
-            float4 va[4], vb[4];
+        for (int w = w0; w <= w1; w += 8) {
+            // eight CTAs' parts in flight, added in order
+            float4 va[8], vb[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 va[i] = vb[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (w + i > w1) continue;
                 const int begin = walk.begin_of(w + i);
@@ -340,12 +343,11 @@ __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const
                 vb[i] = __ldcg(reinterpret_cast<const float4*>(from + cb));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 a.x += va[i].x; a.y += va[i].y; a.z += va[i].z; a.w += va[i].w;
                 b.x += vb[i].x; b.y += vb[i].y; b.z += vb[i].z; b.w += vb[i].w;
             }
         }
-        const int64_t orow = static_cast<int64_t>(gt.row0[c.g]) + c.m0 + r;
         if (EPI == kSwiGLU) {
             const int n = c.n0 + ca;
             float h[4] = {silu_mul(a.x, b.x), silu_mul(a.y, b.y), silu_mul(a.z, b.z),
@@ -367,7 +369,7 @@ __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const
                 (c.routed ? fp.hs_routed : fp.hs_shared)[orow * fp8_scale_ld(N) + c.n0 / 128] =
                     static_cast<uint8_t>(byte);
         } else {
-            const float s = row_weight(p, c, orow);
+            const float s = weight;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out_routed) +
                                  (orow + (c.routed ? 0 : p.out_row0_shared)) * N + c.n0;
             if (c.n0 + ca < N)
@@ -729,26 +731,29 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
             // finishes it
             __threadfence();
             epilogue_sync();
-            if (threadIdx.x == 128) {
-                for (int i = 0; i < 2; ++i) {
-                    last_sh[i] = false;
-                    if (pending[i] < 0) continue;
-                    const int first = walk.first_block(pending[i]);
-                    const int blocks = pending[i] < walk.routed_tiles ? walk.kb_routed
-                                                                      : walk.kb_shared;
+            if (warp < 6 && lane == 0) {
+                const int i = warp - 4;         // one tile each
+                const int tile = pending[i];
+                last_sh[i] = false;
+                if (tile >= 0) {
+                    const int first = walk.first_block(tile);
+                    const int blocks = tile < walk.routed_tiles ? walk.kb_routed : walk.kb_shared;
                     const int n = min(first + blocks, walk.end) -
                                   max(first, walk.begin_of(walk.worker));
-                    last_sh[i] = atomicAdd(fp.arrived + pending[i], n) + n == blocks;
+                    last_sh[i] = atomicAdd(fp.arrived + tile, n) + n == blocks;
                 }
                 __threadfence();
             }
             epilogue_sync();
-            for (int i = 0; i < 2; ++i) {
-                if (!last_sh[i] || !ok) continue;
+            // two tiles: four warps each
+            const bool both = last_sh[0] && last_sh[1];
+            const int i = both ? (warp - 4) >> 2 : last_sh[0] ? 0 : 1;
+            if (last_sh[i] && ok) {
                 sg.tile = pending[i];
                 sg.c = walk.tile_coord(sg.tile);
                 sg.num_kb = sg.c.routed ? walk.kb_routed : walk.kb_shared;
-                finish_parts<EPI, SPLIT>(walk, sg, gt, fp, warp - 4);
+                finish_parts<EPI, SPLIT>(walk, sg, gt, fp, both ? warp & 3 : warp - 4,
+                                         both ? 4 : EPI_WARPS);
             }
         }
     }
