@@ -253,8 +253,9 @@ template <int EPI, bool SPLIT> struct Walk {
     }
 };
 
-// The group table, by one warp, 32 groups at a time.  It is read before
-// pdl_wait, hence from L2: a line of an earlier plan may still be in L1.
+// The group table, by one warp, 32 groups at a time, from the offsets that all
+// threads have put in gt.tile_start[0..E] (an entry is read before the prefix
+// takes its place).
 __device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p, int tile_rows) {
     const int lane = threadIdx.x & 31;
     int start = 0;
@@ -264,8 +265,8 @@ __device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p,
         if (g < p.E) {
             // kept inside the slots, whatever the offsets say
             const int slots = static_cast<int>(p.T * p.k);
-            row0 = min(max(__ldcg(p.offsets + g), 0), slots);
-            rows = max(min(__ldcg(p.offsets + g + 1), slots) - row0, 0);
+            row0 = min(max(gt.tile_start[g], 0), slots);
+            rows = max(min(gt.tile_start[g + 1], slots) - row0, 0);
         } else if (g < p.E + p.S) {
             row0 = static_cast<int>((g - p.E) * p.T);
             rows = static_cast<int>(p.T);
@@ -278,11 +279,13 @@ __device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p,
             const int v = __shfl_up_sync(0xffffffffu, sum, d);
             if (lane >= d) sum += v;
         }
+        __syncwarp();                  // this chunk's offsets are read
         if (g < p.E + p.S) {
             gt.rows[g] = rows;
             gt.row0[g] = row0;
             gt.tile_start[g] = start + sum - tiles;
         }
+        __syncwarp();
         start += __shfl_sync(0xffffffffu, sum, 31);
     }
     if (lane == 0) {
@@ -414,7 +417,8 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     // pdl_wait: what the kernels before the previous one wrote (the plan) and
     // the weights are there already, so the table is built and the first weight
     // tiles are loaded while the previous kernel still runs.
-    if (warp == 0) build_table(gt, p, ROWS);
+    // (The plan is read from L2: a line of an earlier one may still be in L1.)
+    for (int g = threadIdx.x; g <= p.E; g += THREADS) gt.tile_start[g] = __ldcg(p.offsets + g);
     if (threadIdx.x == 32) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -443,6 +447,8 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (warp == 0) build_table(gt, p, ROWS);
+    __syncthreads();
     const uint32_t tmem_base = tmem_base_sh;
     Walk<EPI, SPLIT> walk(gt, p);
     Segment sg;
