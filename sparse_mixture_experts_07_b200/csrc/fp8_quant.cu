@@ -146,6 +146,7 @@ struct QuantRowsParams {
     const uint4* x;
     const int32_t* perm;
     const int32_t* inv;
+    const int32_t* placed;     // offsets[E]: slots that the plan placed
     int64_t T, slots;
     int k, S, H;
     uint8_t* xq;
@@ -153,6 +154,12 @@ struct QuantRowsParams {
     int32_t* arrived;
     int counters;
 };
+
+// Rows that hold a slot: a plan with skipped slots (bad expert index) leaves
+// the rest of perm unset, with whatever an earlier plan put there.
+__device__ __forceinline__ int placed_slots(const int32_t* placed, int64_t slots) {
+    return min(max(*placed, 0), static_cast<int>(slots));
+}
 
 template <bool BY_TOKEN>
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantRowsParams p) {
@@ -163,6 +170,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantRowsP
     const int64_t total = (BY_TOKEN ? p.T : p.slots + (p.S > 0 ? p.T : 0)) * per_row;
     pdl_wait();
     pdl_launch_dependents();     // after the wait: see the GEMM's prologue
+    const int placed = BY_TOKEN ? placed_slots(p.placed, p.slots) : 0;
     if (!BY_TOKEN)
         for (int i = blockIdx.x * 256 + threadIdx.x; i < p.counters; i += gridDim.x * 256)
             p.arrived[i] = 0;
@@ -205,8 +213,8 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantRowsP
                 const int64_t slot = token * p.k + j;
                 const int32_t at = p.inv[slot];
                 // a slot that the plan skipped has no entry: whatever is there
-                // does not lead back to it
-                if (at >= 0 && at < p.slots && p.perm[at] == slot) write(at);
+                // leads to no placed row, or to another slot's
+                if (at >= 0 && at < placed && p.perm[at] == slot) write(at);
             }
             if (p.S > 0) write(p.slots + token);
         } else {
@@ -215,15 +223,17 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantRowsP
     }
 }
 
-// inv[perm[p]] = p.
-__global__ void __launch_bounds__(256) fp8_invert_kernel(const int32_t* perm, int32_t* inv,
-                                                         int64_t n) {
+// inv[perm[p]] = p, over the placed rows.
+__global__ void __launch_bounds__(256) fp8_invert_kernel(const int32_t* perm,
+                                                         const int32_t* placed, int32_t* inv,
+                                                         int64_t slots) {
     pdl_wait();
     pdl_launch_dependents();
+    const int n = placed_slots(placed, slots);
     for (int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; p < n;
          p += static_cast<int64_t>(gridDim.x) * 256) {
         const int32_t q = perm[p];
-        if (q >= 0 && q < n) inv[q] = static_cast<int32_t>(p);
+        if (q >= 0 && q < slots) inv[q] = static_cast<int32_t>(p);
     }
 }
 
@@ -248,14 +258,14 @@ cudaError_t launch_fp8_quantize_rows(const moe_shape& s, const Fp8Operands& o, i
                                      cudaStream_t st) {
     const Fp8Tiles tiles = fp8_tiles(s);
     const bool by_token = fp8_by_token(s);
-    const QuantRowsParams p{static_cast<const uint4*>(o.x), o.perm, o.inv, s.T, s.T * s.k, s.k,
-                            s.n_shared, s.H, o.xq, o.xs, o.arrived,
+    const QuantRowsParams p{static_cast<const uint4*>(o.x), o.perm, o.inv, o.offsets + s.E, s.T,
+                            s.T * s.k, s.k, s.n_shared, s.H, o.xq, o.xs, o.arrived,
                             fp8_is_split(s) ? static_cast<int>(tiles.gate_up + tiles.down) : 0};
     const int64_t most = static_cast<int64_t>(num_sms) * 8;
     auto grid_for = [&](int64_t ctas) { return dim3(static_cast<unsigned>(ctas < most ? ctas : most)); };
     if (by_token) {
         const cudaError_t e = launch_pdl(fp8_invert_kernel, grid_for((p.slots + 255) / 256),
-                                         dim3(256), 0, st, o.perm, o.inv, p.slots);
+                                         dim3(256), 0, st, o.perm, p.placed, o.inv, p.slots);
         if (e != cudaSuccess) return e;
     }
     const int blocks = (s.H + kFp8Block - 1) / kFp8Block;

@@ -491,3 +491,34 @@ def test_replays_follow_the_routing(cuda_ok, T):
             static.copy_(x)
             assert torch.equal(graph.replay(), w)
     assert layer.device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,S", [(20, 0), (40, 1), (300, 2)])
+def test_slots_that_the_plan_skipped(cuda_ok, T, S):
+    """A plan that skipped slots defines perm[0 .. offsets[E]) only.  Whatever the
+    rest of it holds, an earlier plan's slots here, each named by a placed row too,
+    the placed rows are as with nothing there, and (whole tiles: no sums whose
+    parts move with the rows) as in the plan without skips, bit for bit."""
+    E, k = 6, 3
+    shape, x, perm, offsets, w, fp8 = _setup(T, 272, 144, E, k, S, 80 if S else 0, seed=13)
+    full = _run(shape, x, perm, offsets, w, fp8)
+    expert = torch.bucketize(torch.arange(T * k), offsets[1:].long(), right=True)
+    kept = torch.arange(T * k) % 7 != 2
+    kept[offsets[3]:offsets[3] + 2] = False
+    n = int(kept.sum())
+    assert n < T * k - T // 4
+    skipped = torch.cat([perm[kept], perm[kept].flip(0)[:T * k - n]])
+    counts = torch.bincount(expert[kept], minlength=E)
+    short = torch.zeros(E + 1, dtype=torch.int32)
+    short[1:] = counts.cumsum(0)
+    bare = torch.cat([perm[kept], torch.full((T * k - n,), -1, dtype=torch.int32)])
+    want = _run(shape, x, bare, short, w, fp8)
+    if T > 32:
+        assert torch.equal(want[:n], full[:T * k][kept.cuda()])
+        assert torch.equal(want[T * k:], full[T * k:])
+    for fill in (0x00, 0xFF):
+        ws = torch.full((moe.fp8_workspace_size(shape),), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(3):
+            got = _run(shape, x, skipped, short, w, fp8, workspace=ws)
+            assert torch.equal(got[:n], want[:n]) and torch.equal(got[T * k:], want[T * k:])
