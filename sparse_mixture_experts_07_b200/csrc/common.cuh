@@ -90,6 +90,16 @@ __device__ __forceinline__ void stage_offsets(int32_t* dst, const int32_t* offse
 }
 using GroupTable = GroupTableT<kMaxGroups>;
 
+// Rows that hold a slot, *placed = offsets[E] of them: a plan with skipped slots
+// (bad expert index) leaves the rest of perm unset, with whatever an earlier
+// plan put there.
+__device__ __forceinline__ int placed_slots(const int32_t* placed, int64_t slots) {
+    return min(max(*placed, 0), static_cast<int>(slots));
+}
+// inv[perm[p]] = p over those rows (combine.cu).
+cudaError_t launch_invert_perm(const int32_t* perm, const int32_t* placed, int32_t* inv,
+                               int64_t slots, int num_sms, cudaStream_t st);
+
 // ---------------------------------------------------------------------------
 // PTX wrappers (sm_100a).
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

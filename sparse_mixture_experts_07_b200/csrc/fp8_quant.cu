@@ -155,12 +155,6 @@ struct QuantRowsParams {
     int counters;
 };
 
-// Rows that hold a slot: a plan with skipped slots (bad expert index) leaves
-// the rest of perm unset, with whatever an earlier plan put there.
-__device__ __forceinline__ int placed_slots(const int32_t* placed, int64_t slots) {
-    return min(max(*placed, 0), static_cast<int>(slots));
-}
-
 template <bool BY_TOKEN>
 __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantRowsParams p) {
     const int blocks = (p.H + kFp8Block - 1) / kFp8Block;
@@ -223,20 +217,6 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const QuantRowsP
     }
 }
 
-// inv[perm[p]] = p, over the placed rows.
-__global__ void __launch_bounds__(256) fp8_invert_kernel(const int32_t* perm,
-                                                         const int32_t* placed, int32_t* inv,
-                                                         int64_t slots) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int n = placed_slots(placed, slots);
-    for (int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; p < n;
-         p += static_cast<int64_t>(gridDim.x) * 256) {
-        const int32_t q = perm[p];
-        if (q >= 0 && q < slots) inv[q] = static_cast<int32_t>(p);
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_fp8_quantize_weights(const void* w, bool bf16, int64_t n, int rows, int cols,
@@ -264,8 +244,7 @@ cudaError_t launch_fp8_quantize_rows(const moe_shape& s, const Fp8Operands& o, i
     const int64_t most = static_cast<int64_t>(num_sms) * 8;
     auto grid_for = [&](int64_t ctas) { return dim3(static_cast<unsigned>(ctas < most ? ctas : most)); };
     if (by_token) {
-        const cudaError_t e = launch_pdl(fp8_invert_kernel, grid_for((p.slots + 255) / 256),
-                                         dim3(256), 0, st, o.perm, p.placed, o.inv, p.slots);
+        const cudaError_t e = launch_invert_perm(o.perm, p.placed, o.inv, p.slots, num_sms, st);
         if (e != cudaSuccess) return e;
     }
     const int blocks = (s.H + kFp8Block - 1) / kFp8Block;

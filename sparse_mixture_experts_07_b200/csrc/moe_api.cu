@@ -71,8 +71,8 @@ cudaError_t launch_backward(const moe_shape&, const void*, const float*, const i
                             int32_t*, int, cudaStream_t);
 cudaError_t launch_gather_rows(const moe_shape&, const void*, const int32_t*, void*, int,
                                cudaStream_t);
-cudaError_t launch_gather_by_token(const moe_shape&, const void*, const int32_t*, int32_t*, void*,
-                                   int, cudaStream_t);
+cudaError_t launch_gather_by_token(const moe_shape&, const void*, const int32_t*, const int32_t*,
+                                   int32_t*, void*, int, cudaStream_t);
 
 // Host-side validation shared by every entry point (declared in common.cuh).
 moe_status check_shape(const moe_shape* s) {
@@ -401,7 +401,7 @@ moe_status forward_range(const moe_shape& s, int e_begin, int e_end, bool with_s
     const bool by_token = static_cast<int64_t>(s.T) * s.H * 2 > (int64_t(48) << 20);
     if (any_routed) {
         cudaError_t e = by_token
-                            ? moe::launch_gather_by_token(s, x, perm,
+                            ? moe::launch_gather_by_token(s, x, perm, offsets + s.E,
                                                           reinterpret_cast<int32_t*>(ws + w.inv_off),
                                                           x_perm, sms, cs)
                             : moe::launch_gather_rows(s, x, perm, x_perm, sms, cs);

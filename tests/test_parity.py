@@ -329,3 +329,44 @@ def test_permute_plans_match_the_oracle(cuda_ok, T, k, E, skew):
     assert np.array_equal(offsets.cpu().numpy(), o_offsets)
     assert np.array_equal(perm.cpu().numpy(), o_perm)
     assert np.array_equal(inv.cpu().numpy(), o_inv)
+
+
+def test_forward_with_slots_that_the_plan_skipped(cuda_ok):
+    """A prompt whose rows are gathered token by token (more than 48 MB of x),
+    with a plan that skipped slots and so defines perm[0 .. offsets[E]) only:
+    whatever the rest of perm and the workspace hold, the placed rows are as in
+    the plan without skips, bit for bit."""
+    import sparse_mixture_experts_07_b200 as moe
+    T, H, I, E, k = 6400, 4096, 64, 4, 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    shape = moe.Shape(T=T, H=H, I=I, E=E, k=k)
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    gate_up = (torch.randn(E, 2 * I, H, generator=g, device="cuda") / 64).to(torch.bfloat16)
+    down = (torch.randn(E, H, I, generator=g, device="cuda") / 8).to(torch.bfloat16)
+    w = torch.rand(T, k, generator=g, device="cuda")
+    idx = torch.randint(0, E, (T * k,), generator=g, device="cuda")
+
+    def plan(idx):
+        perm = torch.sort(idx, stable=True).indices.to(torch.int32)
+        offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        offsets[1:] = torch.bincount(idx, minlength=E + 1)[:E].cumsum(0)
+        return perm, offsets
+
+    def run(perm, offsets, fill):
+        ws = torch.full((moe.workspace_size(shape),), fill, dtype=torch.uint8, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        y = moe.forward(shape, x, offsets, perm, w, gate_up, down, None, None, ws, err)
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        return y
+    perm, offsets = plan(idx)
+    want = run(perm, offsets, 0)
+    bad = torch.arange(T * k, device="cuda") % 5 == 1
+    short, short_offsets = plan(torch.where(bad, E, idx))     # the skipped slots come last
+    n = int(short_offsets[E])
+    assert n == T * k - int(bad.sum())
+    want = want[:T * k][~bad[perm.long()]]
+    for fill in (0x00, 0x11, 0xFF):
+        short[n:] = short[:T * k - n]                         # each named by a placed row too
+        for _ in range(3):
+            assert torch.equal(run(short, short_offsets, fill)[:n], want)
