@@ -106,6 +106,8 @@ MOE_API moe_status moe_workspace_size(const moe_shape* shape, size_t* bytes);
  *   topk_idx    [T, k]  int32 output: the k largest logits of each token in
  *                       descending order; equal logits go to the lower index
  *   topk_w      [T, k]  float32 output: softmax over the k selected logits
+ *                       (a token whose logits are NaN: k distinct experts in
+ *                       range, NaN weights)
  *   err_flag    [1]     int32 device word, or NULL (see conventions)
  * Logits accumulate in float32.  Up to 256 tokens run on the CUDA cores, a
  * cluster of 8 CTAs per 16 tokens splitting H (one CTA per token where that

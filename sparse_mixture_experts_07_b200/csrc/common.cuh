@@ -90,6 +90,13 @@ __device__ __forceinline__ void stage_offsets(int32_t* dst, const int32_t* offse
 }
 using GroupTable = GroupTableT<kMaxGroups>;
 
+// The routers' arg-max compares scores with a NaN taken as an infinity: every
+// comparison then has an answer, and every round finds an expert.  (A token
+// whose logits are NaN gets the first experts, and NaN weights.)
+__device__ __forceinline__ float nan_as_infinity(float v) {
+    return v == v ? v : __int_as_float(0x7f800000);
+}
+
 // Rows that hold a slot, *placed = offsets[E] of them: a plan with skipped slots
 // (bad expert index) leaves the rest of perm unset, with whatever an earlier
 // plan put there.

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(
             const int e = lane + 32 * j;
             l[j] = acc[t][j] + ((bias && e < E) ? bias[e] : 0.f);
             if (logits && e < E) logits[tok * E + e] = l[j];
+            l[j] = nan_as_infinity(l[j]);
         }
         float sel_v[kMaxK];
         int sel_e[kMaxK];
@@ -152,8 +153,9 @@ __device__ __forceinline__ void select_topk_warp(const float* lg, int E, int k, 
         for (int e = lane; e < E; e += 32) {
             bool taken = false;
             for (int q = 0; q < r; ++q) taken |= (sel_e[q] == e);
-            if (!taken && (lg[e] > best || best_e == 0x7fffffff)) {
-                best = lg[e];
+            const float v = nan_as_infinity(lg[e]);
+            if (!taken && (v > best || best_e == 0x7fffffff)) {
+                best = v;
                 best_e = e;
             }
         }

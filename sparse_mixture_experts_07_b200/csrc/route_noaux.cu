@@ -14,6 +14,7 @@
 namespace moe {
 
 constexpr int kNxWarps = 8;
+constexpr int kNone = 1 << 30;   // index of a lane that has nothing to offer
 
 __device__ __forceinline__ void warp_argmax(float& v, int& i) {
 #pragma unroll
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(kNxWarps * 32) route_noaux_kernel(
         c[i] = ninf;
         if (e < E) {
             const float s = 1.f / (1.f + expf(-logits[t * E + e]));
-            c[i] = s + (bias ? bias[e] : 0.f);
+            c[i] = nan_as_infinity(s + (bias ? bias[e] : 0.f));
             c_sh[warp][e] = c[i];
             s_sh[warp][e] = s;
         }
@@ -64,13 +65,15 @@ __global__ void __launch_bounds__(kNxWarps * 32) route_noaux_kernel(
                 b2 = v;
             }
         }
-        gs = gsize >= 2 ? b1 + b2 : b1;
+        gs = nan_as_infinity(gsize >= 2 ? b1 + b2 : b1);
     }
-    // keep the topk_group best groups
+    // keep the topk_group best groups (a group at -infinity still goes before
+    // the lanes that have none to offer)
     bool keep = false;
     for (int r = 0; r < topk_group; ++r) {
-        float v = (lane < n_group && !keep) ? gs : ninf;
-        int g = lane < n_group ? lane : 1 << 30;
+        const bool offers = lane < n_group && !keep;
+        float v = offers ? gs : ninf;
+        int g = offers ? lane : kNone;
         warp_argmax(v, g);
         if (lane == g) keep = true;
     }
@@ -81,11 +84,12 @@ __global__ void __launch_bounds__(kNxWarps * 32) route_noaux_kernel(
     int sel_j = 0;
     for (int j = 0; j < k; ++j) {
         float v = ninf;
-        int bi = 1 << 30;
+        int bi = kNone;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = lane + 32 * i;
-            if (e < E && !((taken >> i) & 1u) && ((kept >> (e / gsize)) & 1u) && c[i] > v) {
+            if (e < E && !((taken >> i) & 1u) && ((kept >> (e / gsize)) & 1u) &&
+                (c[i] > v || bi == kNone)) {
                 v = c[i];
                 bi = e;
             }

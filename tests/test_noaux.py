@@ -94,3 +94,38 @@ def test_noaux_full_size_dsv3(cuda_ok):
     _, offsets, perm, _ = oracle.permute(o_idx, cfg.E)
     toks = stratified_tokens(o_idx, offsets, perm, 1024)
     _check(cfg, host, layer, y, tokens=toks)
+
+
+@pytest.mark.parametrize("T,E,k,n_group,topk_group", [
+    (1, 8, 4, 4, 2), (5, 64, 6, 8, 4), (40, 32, 4, 1, 1), (300, 16, 3, 4, 2), (70, 256, 8, 32, 8),
+    (9, 16, 16, 4, 4), (9, 8, 2, 8, 2)])
+def test_scores_that_are_not_finite(T, E, k, n_group, topk_group):
+    """A token whose logits are NaN, and experts that a bias of -infinity masks
+    out, one of their groups left whole: k distinct experts in range for each
+    token, the healthy tokens' as the oracle selects them."""
+    import sparse_mixture_experts_07_b200 as moe
+    H, size = 64, E // n_group
+    g = torch.Generator().manual_seed(E)
+    shape = moe.Shape(T=T, H=H, I=64, E=E, k=k)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    wr = torch.randn(E, H, generator=g).cuda()
+    clean = moe.route_noaux_tc(shape, x, wr, None, n_group, topk_group)[:2]
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[T // 2::3] = True
+    x2 = x.clone()
+    x2[bad] = float("nan")
+    idx, w, _ = moe.route_noaux_tc(shape, x2, wr, None, n_group, topk_group)
+    torch.cuda.synchronize()
+    assert torch.equal(idx[~bad], clean[0][~bad]) and torch.equal(w[~bad], clean[1][~bad])
+    assert torch.equal(idx[bad].long(), torch.arange(k, device="cuda").expand(int(bad.sum()), k))
+    assert w[bad].isnan().all()
+    for first in (0, E - size):                       # the group that stays open
+        bias = torch.full((E,), -float("inf"), device="cuda")
+        bias[first:first + size] = 0.5
+        idx, w, _ = moe.route_noaux_tc(shape, x, wr, bias, n_group, topk_group)
+        torch.cuda.synchronize()
+        assert idx.min() >= 0 and idx.max() < E
+        for row in idx.tolist():
+            assert len(set(row)) == k
+            m = min(k, size)
+            assert all(first <= e < first + size for e in row[:m])

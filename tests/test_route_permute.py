@@ -91,3 +91,44 @@ def test_route_permute_sweep_one_launch(case):
     assert np.array_equal(inv[perm], np.arange(T * k))
     keys = sel[perm].astype(np.int64) * (T * k) + perm
     assert np.all(np.diff(keys) > 0)
+
+
+@pytest.mark.parametrize("T,E,k,dtype", [
+    (1, 8, 2, "bf16"), (5, 64, 6, "bf16"), (16, 4, 4, "bf16"), (16, 33, 16, "f32"),   # one launch
+    (17, 8, 2, "bf16"), (100, 256, 8, "bf16"), (100, 16, 3, "f32"),
+    (300, 16, 2, "bf16"), (300, 128, 4, "bf16"), (300, 8, 8, "f32")])
+def test_tokens_that_are_not_finite(T, E, k, dtype):
+    """A token whose logits are NaN gets k distinct experts and NaN weights; the
+    plan stays a permutation, and the other tokens' selections are as without it."""
+    import sparse_mixture_experts_07_b200 as moe
+    H = 128
+    g = torch.Generator().manual_seed(T + E)
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    shape = moe.Shape(T=T, H=H, I=64, E=E, k=k,
+                      dtype=moe.MOE_BF16 if dtype == "bf16" else moe.MOE_F32)
+    x = torch.randn(T, H, generator=g).to(td).cuda()
+    wr = torch.randn(E, H, generator=g).cuda()
+    ws = moe.alloc_workspace(shape)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    clean = moe.route_permute(shape, x, wr, None, ws, err)[:2]
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[::3] = True
+    x[bad] = float("nan")
+    idx, w, _, counts, offsets, perm, inv = moe.route_permute(shape, x, wr, None, ws, err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    assert torch.equal(idx[~bad], clean[0][~bad]) and torch.equal(w[~bad], clean[1][~bad])
+    assert torch.equal(idx[bad].long(), torch.arange(k, device="cuda").expand(int(bad.sum()), k))
+    assert w[bad].isnan().all()
+    for got, want in zip((counts, offsets, perm, inv), oracle.permute(idx.cpu().numpy(), E)):
+        assert np.array_equal(got.cpu().numpy(), want)
+    # experts that a bias of -infinity masks out
+    x = torch.randn(T, H, generator=g).to(td).cuda()
+    bias = torch.zeros(E, device="cuda")
+    bias[E // 2:] = -float("inf")
+    idx, w, *_ = moe.route_permute(shape, x, wr, bias, ws, err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and idx.min() >= 0 and idx.max() < E
+    assert all(len(set(row)) == k for row in idx.tolist())
+    if k <= E // 2:
+        assert idx.max() < E // 2 and w.isfinite().all()
