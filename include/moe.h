@@ -194,8 +194,12 @@ MOE_API moe_status moe_route_noaux_tc(const moe_shape* shape, int32_t n_group,
  *                     (expert ascending, slot id ascending) - deterministic
  *   inv       [T*k]   int32 output: sorted position of slot q (perm^-1)
  *   err_flag  [1]     int32, OR-ed with 1 << MOE_ERR_BAD_INDEX if an index is
- *                     outside [0, E); such slots are skipped and the outputs
- *                     are then unspecified (all writes stay in bounds)
+ *                     outside [0, E); such slots are skipped: the plan is that
+ *                     of the others, with inv[q] = -1 for the skipped slots
+ *                     and perm[p] = -1 for p >= offsets[E].  The combines then
+ *                     sum the token's other slots; unspecified are the rows
+ *                     of y_slots from offsets[E] to T*k and moe_backward's
+ *                     gradients (all accesses stay in bounds)
  *   workspace         at least moe_workspace_size() bytes */
 MOE_API moe_status moe_permute(const moe_shape* shape, const int32_t* topk_idx, int32_t* counts,
                        int32_t* offsets, int32_t* perm, int32_t* inv, int32_t* err_flag,
@@ -540,7 +544,7 @@ MOE_API moe_status moe_forward_fp8(const moe_shape* shape, const void* x, const 
  *   moe_norm_backward_workspace_size() bytes, 16-byte aligned.
  *
  * All three use T, H, k, n_shared and dtype of `shape`, H <= 32768; slots
- * whose entry of inv lies outside [0, T*k) (a plan with bad indices) add
+ * whose entry of inv lies outside [0, T*k) (-1: skipped by moe_permute) add
  * nothing.  float32 rows may have any H and alignment. */
 typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2 } moe_gate_kind;

@@ -246,7 +246,9 @@ __global__ void __launch_bounds__(kBwdThreads) dx_combine_kernel(
         if (threadIdx.x < k) {
             const int64_t q = t * k + threadIdx.x;
             const int e = topk_idx[q];
-            rows_sh[threadIdx.x] = static_cast<int64_t>(inv[q]) - offsets[e] + poffsets[e];
+            // -1: a slot that the plan skipped, which adds nothing
+            rows_sh[threadIdx.x] =
+                e >= 0 && e < E ? static_cast<int64_t>(inv[q]) - offsets[e] + poffsets[e] : -1;
         }
         for (int e = threadIdx.x; e < E; e += kBwdThreads) dl_sh[e] = dl[t * E + e];
         __syncthreads();
@@ -262,7 +264,8 @@ __global__ void __launch_bounds__(kBwdThreads) dx_combine_kernel(
                     acc[2 * i + 1] += bf16_to_f32(static_cast<uint16_t>(w[i] >> 16));
                 }
             };
-            for (int j = 0; j < k; ++j) add_row(dX[rows_sh[j] * vpr + v]);
+            for (int j = 0; j < k; ++j)
+                if (rows_sh[j] >= 0) add_row(dX[rows_sh[j] * vpr + v]);
             for (int s = 0; s < S; ++s) add_row(dX_sh[(static_cast<int64_t>(s) * T + t) * vpr + v]);
             for (int e = 0; e < E; ++e) {
                 const float g = dl_sh[e];

@@ -16,6 +16,12 @@
 
 namespace moe {
 
+// The row of y_slots that a slot's entry of inv names, -1 for a slot that the
+// plan skipped: it adds nothing.
+__device__ __forceinline__ int64_t slot_row(int32_t at, int64_t routed_rows) {
+    return at >= 0 && at < routed_rows ? at : -1;
+}
+
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ y_slots,
                                                       const int32_t* __restrict__ inv,
@@ -24,13 +30,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ y_sl
     const int64_t routed_rows = n_tokens * k;
     for (int64_t t = blockIdx.x; t < n_tokens; t += gridDim.x) {
         int64_t rows[kMaxK + kMaxShared];
-        for (int j = 0; j < k; ++j) rows[j] = inv[t * k + j];
+        for (int j = 0; j < k; ++j) rows[j] = slot_row(inv[t * k + j], routed_rows);
         for (int s = 0; s < S; ++s) rows[k + s] = routed_rows + s * n_tokens + t;
         for (int c = threadIdx.x * VEC; c < H; c += 256 * VEC) {
             float acc[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) acc[v] = 0.f;
             for (int j = 0; j < k + S; ++j) {
+                if (rows[j] < 0) continue;
                 const T* src = y_slots + rows[j] * H + c;
                 if constexpr (VEC == 4) {
                     const float4 u = *reinterpret_cast<const float4*>(src);
@@ -68,7 +75,7 @@ __global__ void __launch_bounds__(256) combine_bf16_pipelined_kernel(
     __shared__ int64_t rows_sh[2][kMaxK + kMaxShared];
     int buf = 0;
     for (; t < n_tokens; t += gridDim.x) {
-        if (static_cast<int>(threadIdx.x) < k) rows_sh[buf][threadIdx.x] = next_idx;
+        if (static_cast<int>(threadIdx.x) < k) rows_sh[buf][threadIdx.x] = slot_row(next_idx, routed_rows);
         if (static_cast<int>(threadIdx.x) < S)
             rows_sh[buf][k + threadIdx.x] = routed_rows + threadIdx.x * n_tokens + t;
         __syncthreads();
@@ -84,7 +91,10 @@ __global__ void __launch_bounds__(256) combine_bf16_pipelined_kernel(
                 uint4 u[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (r < n) u[r] = y_slots[rows_sh[buf][j + r] * vec_per_row + v];
+                    if (r < n) {
+                        const int64_t row = rows_sh[buf][j + r];
+                        u[r] = row >= 0 ? y_slots[row * vec_per_row + v] : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     if (r >= n) break;

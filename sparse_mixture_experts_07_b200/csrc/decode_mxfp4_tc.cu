@@ -602,7 +602,8 @@ __device__ __forceinline__ bool pad_scale_block(int64_t r, int blk, int K, int S
     return true;
 }
 
-// GEMM 1 operand B: x[perm[r] / k] of every sorted slot row r.
+// GEMM 1 operand B: x[perm[r] / k] of every sorted slot row r (-1: a place that
+// the plan left empty; no expert reads the row).
 __global__ void __launch_bounds__(mxtc::PREP_THREADS) mx_tc_prep_x_kernel(
     const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ perm, int k, int K, int SP,
     int sf_rows, uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(mxtc::PREP_THREADS) mx_tc_prep_x_kernel(
     const int r = blockIdx.y;
     const int blk = blockIdx.x * (mxtc::PREP_THREADS / 32) + (threadIdx.x >> 5);
     if (pad_scale_block(r, blk, K, SP, sf_rows, sf)) return;
-    const int64_t tok = perm[r] / k;
+    const int64_t tok = max(perm[r], 0) / k;
     const float v = __bfloat162float(x[tok * K + blk * 32 + (threadIdx.x & 31)]);
     store_e4m3_pair(v, r, blk, K, SP, sf_rows, q, sf);
 }
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(256) mx_tc_down_out_kernel(
     const int splits = ctl[0];
     float acc = 0.f;
     for (int s = 0; s < splits; ++s) acc += part[(static_cast<int64_t>(s) * S + r) * H + n];
-    const float w = routed_scale * topk_w[perm[r]];
+    const float w = routed_scale * topk_w[max(perm[r], 0)];
     y_slots[static_cast<int64_t>(r) * H + n] = __float2bfloat16_rn(w * acc);
 }
 

@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 5 : MAXT == 512 ? 2 : 1)
     pdl_launch_dependents();
     pdl_wait();
     // lane j holds the row of slot j, k + S <= 24 of them; the next token's are
-    // fetched while this one is worked on.  A plan with skipped slots (bad expert
-    // index) leaves holes: -1, a slot that adds nothing.
+    // fetched while this one is worked on.  -1: a slot that the plan skipped (bad
+    // expert index), which adds nothing.
     auto slot_row = [&](int64_t t) {
         int64_t row = -1;
         if (t < p.T && lane < p.k) {

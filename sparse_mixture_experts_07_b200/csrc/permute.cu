@@ -14,7 +14,9 @@
 //   3. scatter: each block ranks its slots stably (warp match + per-warp
 //      counts, rounds in slot order) and writes perm and inv.
 // The order (expert ascending, slot ascending) is fixed, so the plan is
-// bit-identical run to run.  Workspace: nblocks * E int32.
+// bit-identical run to run.  A slot whose expert index is out of range gets no
+// place: its entry of inv and the places left over in perm are -1, whatever an
+// earlier plan put into the buffers.  Workspace: nblocks * E int32.
 //
 // Up to 8 * 8 * 1024 slots, the plan runs instead as ONE launch on one
 // thread-block cluster of up to 8 CTAs of 1024 threads (permute_cluster_kernel):
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kPermThreads) permute_scan_kernel(
 
 __global__ void __launch_bounds__(kPermThreads) permute_scatter_kernel(
     const int32_t* __restrict__ idx, int64_t n, int E, const int32_t* __restrict__ blk_base,
-    int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
+    const int32_t* __restrict__ offsets, int32_t* __restrict__ perm, int32_t* __restrict__ inv) {
     __shared__ int32_t running[2][kMaxExperts];
     // per-warp counts of the current round, stamped with the round in the high
     // half so that entries left from earlier rounds read as zero
@@ -107,6 +109,9 @@ __global__ void __launch_bounds__(kPermThreads) permute_scatter_kernel(
         running[0][e] = blk_base[static_cast<int64_t>(blockIdx.x) * E + e];
     for (int i = tid; i < (kPermThreads / 32) * kMaxExperts; i += kPermThreads)
         (&wcnt[0][0])[i] = -1;
+    for (int64_t p = offsets[E] + static_cast<int64_t>(blockIdx.x) * kPermThreads + tid; p < n;
+         p += static_cast<int64_t>(gridDim.x) * kPermThreads)
+        perm[p] = -1;
     const int64_t base = static_cast<int64_t>(blockIdx.x) * kPermSlotsPerBlock;
     int ev[kPermRounds];
 #pragma unroll
@@ -133,6 +138,8 @@ __global__ void __launch_bounds__(kPermThreads) permute_scatter_kernel(
             }
             perm[p] = static_cast<int32_t>(q);
             inv[q] = p;
+        } else if (q < n) {
+            inv[q] = -1;
         }
         for (int ee = tid; ee < E; ee += kPermThreads) {
             int32_t sum = 0;
@@ -164,6 +171,7 @@ __global__ void __launch_bounds__(kPcThreads, 1) permute_cluster_kernel(
     // half so that entries left from earlier rounds read as zero
     __shared__ int32_t wcnt[kPcWarps][kMaxExperts];
     __shared__ int32_t warp_sum[kPcWarps];
+    __shared__ int32_t placed;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(cluster_ctarank());
     const int csize = static_cast<int>(gridDim.x);
@@ -222,6 +230,7 @@ __global__ void __launch_bounds__(kPcThreads, 1) permute_cluster_kernel(
         int32_t excl = incl - total;
         for (int w = 0; w < warp; ++w) excl += warp_sum[w];
         running[0][tid] = excl + before_cta;
+        if (tid == E - 1) placed = excl + total;
         if (rank == 0) {
             counts[tid] = total;
             offsets[tid] = excl;
@@ -229,6 +238,10 @@ __global__ void __launch_bounds__(kPcThreads, 1) permute_cluster_kernel(
         }
     }
     __syncthreads();
+
+    for (int64_t p = placed + static_cast<int64_t>(rank) * kPcThreads + tid; p < n;
+         p += static_cast<int64_t>(csize) * kPcThreads)
+        perm[p] = -1;
 
     // stable scatter, rounds in slot order
 #pragma unroll
@@ -248,6 +261,8 @@ __global__ void __launch_bounds__(kPcThreads, 1) permute_cluster_kernel(
             }
             perm[p] = static_cast<int32_t>(q);
             inv[q] = p;
+        } else if (q < hi) {
+            inv[q] = -1;
         }
         for (int ee = tid; ee < E; ee += kPcThreads) {
             int32_t sum = 0;
@@ -330,7 +345,7 @@ cudaError_t launch_permute(const moe_shape& s, const int32_t* idx, int32_t* coun
     permute_scan_kernel<<<1, kPermThreads, 0, st>>>(blk, nblk, s.E, counts, offsets);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || nblk == 0) return e;
-    permute_scatter_kernel<<<nblk, kPermThreads, 0, st>>>(idx, n, s.E, blk, perm, inv);
+    permute_scatter_kernel<<<nblk, kPermThreads, 0, st>>>(idx, n, s.E, blk, offsets, perm, inv);
     return cudaGetLastError();
 }
 

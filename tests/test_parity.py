@@ -370,3 +370,98 @@ def test_forward_with_slots_that_the_plan_skipped(cuda_ok):
         short[n:] = short[:T * k - n]                         # each named by a placed row too
         for _ in range(3):
             assert torch.equal(run(short, short_offsets, fill)[:n], want)
+
+
+def _holed(idx, E):
+    """Every fifth slot out of range, on both sides of it."""
+    bad = torch.arange(idx.numel()) % 5 == 3
+    bad[0] = True
+    out = idx.reshape(-1).clone()
+    out[bad] = torch.tensor([-1, E, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)[
+        torch.arange(int(bad.sum())) % 4]
+    return out.view(idx.shape), bad
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 1, 4), (1, 4, 4), (9, 2, 8), (700, 1, 256), (5001, 3, 64),
+                                   (65537, 1, 32), (30001, 5, 200)])
+def test_plan_of_bad_indices(cuda_ok, T, k, E):
+    """Slots with an index out of range get no place: inv and the rest of perm
+    are -1 whatever the buffers held, everything else is the others' plan."""
+    import sparse_mixture_experts_07_b200 as moe
+    g = torch.Generator().manual_seed(T)
+    idx, bad = _holed(torch.randint(0, E, (T, k), generator=g, dtype=torch.int32), E)
+    shape = moe.Shape(T=T, H=128, I=128, E=E, k=k)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = {name: torch.full((n,), 1, dtype=torch.int32, device="cuda")
+           for name, n in (("counts", E), ("offsets", E + 1), ("perm", T * k), ("inv", T * k))}
+    counts, offsets, perm, inv = (t.cpu() for t in moe.permute(
+        shape, idx.cuda(), moe.alloc_workspace(shape), err, out=out))
+    assert err.item() == 1 << 5
+    n = T * k - int(bad.sum())
+    key = torch.where(bad, E, idx.reshape(-1)).long()
+    order = torch.sort(key, stable=True).indices
+    assert torch.equal(counts.long(), torch.bincount(key, minlength=E + 1)[:E])
+    assert torch.equal(offsets[1:].long(), counts.long().cumsum(0)) and offsets[0] == 0
+    assert torch.equal(perm[:n].long(), order[:n]) and (perm[n:] == -1).all()
+    assert (inv[bad] == -1).all() and torch.equal(inv[order[:n]].long(), torch.arange(n))
+
+
+@pytest.mark.parametrize("weights,T,H,I,E,k", [
+    ("bf16", 5, 256, 128, 8, 2), ("bf16", 60, 256, 128, 8, 2), ("bf16", 900, 256, 128, 3, 2),
+    ("f32", 33, 130, 72, 6, 3), ("f32", 5, 128, 72, 6, 1),
+    ("mxfp4", 1, 256, 128, 8, 2), ("mxfp4", 9, 256, 128, 8, 1), ("mxfp4", 40, 96, 96, 8, 3),
+    ("fp8", 3, 256, 128, 8, 2), ("fp8", 50, 256, 128, 8, 3)])
+def test_block_on_a_plan_of_bad_indices(cuda_ok, weights, T, H, I, E, k):
+    """permute, the experts and both combines in a run on the device's own plan of
+    bad indices: a token is the sum of its other slots, as the whole plan has
+    them.  Each side is rounded at most twice (slots, then y) to 2^-8 of itself
+    (float32: sums of the same terms)."""
+    import sparse_mixture_experts_07_b200 as moe
+    from sparse_mixture_experts_07_b200.inputs import make_mxfp4_weights
+    dtype = "f32" if weights == "f32" else "bf16"
+    cfg = MoEConfig("bad", T=T, H=H, I=I, E=E, k=k, dtype=dtype)
+    d = to_device(make_inputs(cfg))
+    shape = moe.Shape.from_config(cfg)
+    ws = moe.alloc_workspace(shape)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    idx, w, _ = moe.route(shape, d["x"], d["w_router"], d["router_bias"], err_flag=err)
+    if weights == "mxfp4":
+        mx = {n: t.cuda() for n, t in make_mxfp4_weights(cfg).items()}
+        prepared = moe.mxfp4_prepare(shape, mx)
+    elif weights == "fp8":
+        f8 = moe.fp8_experts(d["gate_up"], d["down"])
+
+    def run(idx):
+        plan = {name: torch.full((n,), 1, dtype=torch.int32, device="cuda")
+                for name, n in (("counts", E), ("offsets", E + 1), ("perm", T * k),
+                                ("inv", T * k))}
+        _, offsets, perm, inv = moe.permute(shape, idx, ws, err, out=plan)
+        y = torch.full((shape.slot_rows, H), float("nan"), dtype=shape.torch_dtype,
+                       device="cuda")
+        if weights == "mxfp4" and prepared is not None:
+            moe.forward_mxfp4_prepared(shape, d["x"], offsets, perm, w, mx, prepared, ws, err,
+                                       y_slots=y)
+        elif weights == "mxfp4":
+            moe.forward_mxfp4(shape, d["x"], offsets, perm, w, mx, ws, err, y_slots=y)
+        elif weights == "fp8":
+            moe.forward_fp8(shape, d["x"], offsets, perm, w, f8, err_flag=err, y_slots=y)
+        else:
+            moe.forward(shape, d["x"], offsets, perm, w, d["gate_up"], d["down"], None, None, ws,
+                        err, y_slots=y)
+        h, _, _ = moe.combine_norm(shape, y, inv)
+        out = moe.combine(shape, y, inv)
+        torch.cuda.synchronize()
+        return y, inv, out, h
+    y, inv, _, _ = run(idx)
+    assert err.item() == 0
+    slots = y[inv.long()].view(T, k, H).double()
+    holed, bad = _holed(idx.cpu(), E)
+    slots[bad.view(T, k).cuda()] = 0
+    want = slots.sum(1)
+    assert want.isfinite().all()
+    _, inv, out, h = run(holed.cuda())
+    assert err.item() == 1 << 5 and (inv[bad.cuda()] == -1).all()
+    tol = 1e-5 if dtype == "f32" else 3 * 2.0 ** -8
+    for got in (out, h):
+        assert torch.equal(got[want.abs().sum(1) == 0].abs().sum(), got.new_zeros(()))
+        assert (got.double() - want).norm() <= tol * want.norm()
