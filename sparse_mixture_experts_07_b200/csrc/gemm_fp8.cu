@@ -253,6 +253,19 @@ template <int EPI, bool SPLIT> struct Walk {
     }
 };
 
+// Offsets that do not go up from 0 to at most the slots (no plan of moe_permute's):
+// each is brought into that range and to the smallest behind it.  The groups'
+// rows then lie side by side and end at offsets[E], as the rounding of x takes
+// it, so that rows, tiles and the arrival counters stay within what the host
+// sized, whatever the offsets say.  By one warp.
+__device__ __forceinline__ void order_offsets(int32_t* offsets, int E, int slots) {
+    if ((threadIdx.x & 31) == 0) {
+        int least = slots;
+        for (int g = E; g >= 0; --g) offsets[g] = least = max(min(offsets[g], least), 0);
+    }
+    __syncwarp();
+}
+
 // The group table, by one warp, 32 groups at a time, from the offsets that all
 // threads have put in gt.tile_start[0..E] (an entry is read before the prefix
 // takes its place).
@@ -263,10 +276,8 @@ __device__ __forceinline__ void build_table(GroupTable& gt, const GemmParams& p,
         const int g = g0 + lane;
         int rows = 0, row0 = 0;
         if (g < p.E) {
-            // kept inside the slots, whatever the offsets say
-            const int slots = static_cast<int>(p.T * p.k);
-            row0 = min(max(gt.tile_start[g], 0), slots);
-            rows = max(min(gt.tile_start[g + 1], slots) - row0, 0);
+            row0 = gt.tile_start[g];
+            rows = gt.tile_start[g + 1] - row0;
         } else if (g < p.E + p.S) {
             row0 = static_cast<int>((g - p.E) * p.T);
             rows = static_cast<int>(p.T);
@@ -418,7 +429,14 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
     // the weights are there already, so the table is built and the first weight
     // tiles are loaded while the previous kernel still runs.
     // (The plan is read from L2: a line of an earlier one may still be in L1.)
-    for (int g = threadIdx.x; g <= p.E; g += THREADS) gt.tile_start[g] = __ldcg(p.offsets + g);
+    const int slots = static_cast<int>(p.T * p.k);
+    bool disorder = false;
+    for (int g = threadIdx.x; g <= p.E; g += THREADS) {
+        const int at = __ldcg(p.offsets + g);
+        const int next = g < p.E ? __ldcg(p.offsets + g + 1) : slots;
+        disorder |= at < 0 || at > next || next > slots;
+        gt.tile_start[g] = at;
+    }
     if (threadIdx.x == 32) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -445,9 +463,12 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
         }
     }
     tc_fence_before();
-    __syncthreads();
+    const bool reorder = __syncthreads_or(disorder);
     tc_fence_after();
-    if (warp == 0) build_table(gt, p, ROWS);
+    if (warp == 0) {
+        if (reorder) order_offsets(gt.tile_start, p.E, slots);
+        build_table(gt, p, ROWS);
+    }
     __syncthreads();
     const uint32_t tmem_base = tmem_base_sh;
     Walk<EPI, SPLIT> walk(gt, p);

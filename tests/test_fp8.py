@@ -522,3 +522,26 @@ def test_slots_that_the_plan_skipped(cuda_ok, T, S):
         for _ in range(3):
             got = _run(shape, x, skipped, short, w, fp8, workspace=ws)
             assert torch.equal(got[:n], want[:n]) and torch.equal(got[T * k:], want[T * k:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 32, 100])
+def test_offsets_out_of_order(cuda_ok, T):
+    """Offsets that no plan has (down as well as up, outside the slots): each
+    counts as the smallest from it on, and nothing is written past the workspace
+    or the slot rows."""
+    E, k = 6, 2
+    shape, x, perm, offsets, w, fp8 = _setup(T, 272, 144, E, k, 1, 80, seed=14)
+    n, size = T * k, moe.fp8_workspace_size(shape)
+    for odd in ([0, n, 0, n, 0, n, 0], [-5, 3, 2, 2 ** 31 - 1, 7, -2 ** 31, 1],
+                [n, 1, 2, 3, 4, 5, 6], [0, 1, 1, n - 1, 2, n, n + 1]):
+        got = []
+        for o in (odd, np.minimum.accumulate(np.clip(odd, 0, n)[::-1])[::-1].tolist()):
+            ws = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+            y = torch.full((shape.slot_rows + 2, shape.H), 7.0, dtype=torch.bfloat16,
+                           device="cuda")
+            _run(shape, x, perm, torch.tensor(o, dtype=torch.int32), w, fp8, workspace=ws[:size],
+                 y_slots=y[1:-1])
+            assert (ws[size:] == 0x5A).all() and (y[0] == 7).all() and (y[-1] == 7).all()
+            got.append(y)
+        assert torch.equal(*got)
