@@ -175,13 +175,16 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * rcp_approx(1.f + exp2_approx(g * -1.44269504f)) * u;
 }
 
-// What a row of y is multiplied by (GEMM 2).  A plan with skipped slots (bad
-// expert index) leaves holes in perm.
+// What a row of y is multiplied by (GEMM 2).  `hole`: an entry of perm outside
+// the slots.  No token was rounded into such a row; it is written as zeros
+// (a weight of 0 would keep the NaN that old codes and scales can stand for).
 __device__ __forceinline__ float row_weight(const GemmParams& p, const TileCoord& c,
-                                            int64_t row) {
+                                            int64_t row, bool& hole) {
+    hole = false;
     if (!c.routed) return 1.f;
     const int64_t slot = p.perm[row];
-    return slot >= 0 && slot < p.T * p.k ? p.routed_scale * p.topk_w[slot] : 0.f;
+    hole = slot < 0 || slot >= p.T * p.k;
+    return hole ? 0.f : p.routed_scale * p.topk_w[slot];
 }
 
 // The tiles a CTA computes, in the order that its producer, MMA and epilogue
@@ -341,7 +344,8 @@ __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const
     const int ca = 4 * lane, cb = 128 + 4 * lane;
     for (int r = warp; r < rows; r += warps) {
         const int64_t orow = static_cast<int64_t>(gt.row0[c.g]) + c.m0 + r;
-        const float weight = EPI == kScaled ? row_weight(p, c, orow) : 1.f;
+        bool hole = false;
+        const float weight = EPI == kScaled ? row_weight(p, c, orow, hole) : 1.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
         for (int w = w0; w <= w1; w += 8) {
             // eight CTAs' parts in flight, added in order
@@ -384,6 +388,7 @@ __device__ __forceinline__ void finish_parts(const Walk<EPI, SPLIT>& walk, const
                     static_cast<uint8_t>(byte);
         } else {
             const float s = weight;
+            if (hole) a = b = make_float4(0.f, 0.f, 0.f, 0.f);
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out_routed) +
                                  (orow + (c.routed ? 0 : p.out_row0_shared)) * N + c.n0;
             if (c.n0 + ca < N)
@@ -737,7 +742,9 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
                 }
             } else if (valid && ok) {
                 int64_t orow = static_cast<int64_t>(gt.row0[c.g]) + m;
-                const float scale = row_weight(p, c, orow);
+                bool hole;
+                const float scale = row_weight(p, c, orow, hole);
+                const uint32_t keep = hole ? 0u : 0xffffffffu;
                 if (!c.routed) orow += p.out_row0_shared;
                 const int n = c.n0 + 128 * half;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out_routed) + orow * N + n;
@@ -747,7 +754,7 @@ __global__ void __launch_bounds__(fp8g::THREADS, 1) grouped_gemm_fp8(
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int j = 16 * v + 2 * e;
-                        o[e] = pack_bf16x2(scale * acc[j], scale * acc[j + 1]);
+                        o[e] = pack_bf16x2(scale * acc[j], scale * acc[j + 1]) & keep;
                     }
                     if (n + 16 * v < N) store32(out + 16 * v, o, fp.wide);
                 }

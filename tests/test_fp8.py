@@ -545,3 +545,21 @@ def test_offsets_out_of_order(cuda_ok, T):
             assert (ws[size:] == 0x5A).all() and (y[0] == 7).all() and (y[-1] == 7).all()
             got.append(y)
         assert torch.equal(*got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 4, 32, 100])
+@pytest.mark.parametrize("fill", [0x00, 0x7F, 0xFF])
+def test_holes_are_zero_on_any_workspace(cuda_ok, T, fill):
+    """Rows of holes in perm are zeros whatever the workspace held (0xFF, 0x7F:
+    codes that are NaN, 0xFF a scale that is), the others as without the holes."""
+    shape, x, perm, offsets, w, fp8 = _setup(T, 272, 144, 4, 2, 1, 64, seed=15)
+    y = _run(shape, x, perm, offsets, w, fp8)
+    holed = perm.clone()
+    rows = [0] if T == 1 else [1, 4, 2 * T - 1]
+    holed[rows] = torch.tensor([-1, 2 * T, 2 ** 31 - 1], dtype=torch.int32)[:len(rows)]
+    ws = torch.full((moe.fp8_workspace_size(shape),), fill, dtype=torch.uint8, device="cuda")
+    got = _run(shape, x, holed, offsets, w, fp8, workspace=ws)
+    keep = torch.ones(shape.slot_rows, dtype=torch.bool, device="cuda")
+    keep[rows] = False
+    assert torch.equal(got[keep], y[keep]) and (got[~keep] == 0).all()
