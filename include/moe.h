@@ -579,8 +579,9 @@ MOE_API moe_status moe_norm_backward(const moe_shape* shape, const moe_norm_spec
  *   Ranks that hold different gradients all-reduce it (sum) before clipping.
  * moe_clip_grads: norm [1] float32 (or NULL) = n = sqrt(total), and
  *   g *= c with c = max_norm / (n + 1e-6) where c < 1; nothing is written to
- *   the gradients when c >= 1.  As in the formula, an infinite norm zeroes
- *   finite gradients and a NaN norm makes all of them NaN: read `norm`.
+ *   the gradients when c >= 1 or max_norm is infinite (the call then only
+ *   measures).  Under a finite max_norm, as in the formula, an infinite norm
+ *   zeroes finite gradients and a NaN norm makes all of them NaN: read `norm`.
  * moe_clip_grad_norm: both, on the tensors' own total (one launch less).
  * Squares and sums are float64 in a fixed order (deterministic, no overflow
  * of float32 squares).  Workspace: moe_grad_norm_workspace_size() bytes,

@@ -3,7 +3,7 @@
 //   n = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (n + 1e-6)),
 //   g *= c where c < 1
 // (the clipping step of a training loop, over the gradients that moe_backward
-// writes).  Squares are taken and summed in float64: the square of any float32
+// writes); max_norm = infinity leaves every gradient as it is.  Squares are taken and summed in float64: the square of any float32
 // or bf16 value is a float64 in range, so neither gradients of 1e30 nor of
 // 1e-30 overflow or vanish, and the order of the sum is fixed: chunk by chunk
 // in each thread, threads in a tree, CTAs in order.  No atomics.
@@ -134,7 +134,9 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
     const double n2 = sqrt(sum_parts(part, parts));
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(n2);
     const double ratio = static_cast<double>(max_norm) / (n2 + 1e-6);
-    if (ratio >= 1.0) return;            // a NaN norm goes on and reaches every gradient
+    // an infinite limit only measures, an infinite or NaN norm included; under a
+    // finite one a NaN norm goes on and reaches every gradient
+    if (ratio >= 1.0 || max_norm == __int_as_float(0x7f800000)) return;
     const float c = static_cast<float>(ratio);
     const int64_t chunks = l.chunk_start[l.n];
     for (int64_t at = blockIdx.x; at < chunks; at += gridDim.x) {

@@ -774,3 +774,31 @@ def test_sublayer_without_a_norm_after(cuda_ok, gate):
         assert rel_l2(_np(got["gate"]), gp["gate"]) < 1e-5
     # serving gives the same h'
     assert rel_l2(_np(sub(h.cuda())[0]), _np(h2)) < BF16_TOL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_clip_without_a_limit_only_measures(cuda_ok, bad):
+    """max_norm = infinity returns the norm, infinite or NaN as it may be, and
+    changes no gradient, in one call and in two; a finite one as the formula says."""
+    def grads():
+        g = torch.Generator().manual_seed(3)
+        out = [torch.randn(n, generator=g).to(t).cuda()
+               for n, t in ((5000, torch.float32), (77, torch.bfloat16), (1, torch.float32))]
+        out[0][4321] = bad
+        return out
+    inf, first = float("inf"), grads()
+    for two in (False, True):
+        got = grads()
+        n = moe.clip_grads(got, inf, moe.grad_square_sum(got)) if two else \
+            moe.clip_grad_norm(got, inf)
+        assert n.isnan() if bad != bad else n == inf
+        assert all(torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)) for a, b in zip(got, first))
+        got = grads()
+        n = moe.clip_grads(got, 1.0, moe.grad_square_sum(got)) if two else \
+            moe.clip_grad_norm(got, 1.0)
+        if bad != bad:
+            assert all(t.isnan().all() for t in got)
+        else:
+            assert got[0][4321].isnan() and not got[1].any() and not got[2].any()
+            assert not got[0][:4321].any() and not got[0][4322:].any()
