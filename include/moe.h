@@ -523,7 +523,7 @@ MOE_API moe_status moe_forward_fp8(const moe_shape* shape, const void* x, const 
  *   MOE_NORM_NONE: N(v) = v (weight and bias NULL, eps ignored).
  *   weight, bias: [H] float32 device pointers, NULL for ones / zeros.
  *
- * moe_norm_forward: y = N(x), x and y [T, H] dtype.
+ * moe_norm_forward: y = N(x), x and y [T, H] dtype; y may be x.
  *
  * moe_combine_norm: with v = moe_combine's sum for a token (float32, not
  *   rounded),
@@ -534,12 +534,15 @@ MOE_API moe_status moe_forward_fp8(const moe_shape* shape, const void* x, const 
  *   (MOE_GATE_CHANNEL) float32, NULL with MOE_GATE_NONE; post NULL = no norm;
  *   next and xn_out both NULL = no next norm; y_out [T, H] dtype or NULL:
  *   the combined v, rounded (what moe_norm_backward reads as x).
- *   h_out may be residual itself; other outputs overlap nothing.
+ *   One of the outputs may be residual itself (the same pointer); otherwise
+ *   the outputs overlap neither one another nor y_slots or residual
+ *   (MOE_ERR_INVALID_ARG).
  *
  * moe_norm_backward: gradients of out = scale * gate * N(x) given dout:
  *     dx [T, H] dtype (+ dadd [T, H] dtype when not NULL: the gradient that
  *     reaches x past the norm), dweight [H], dbias [H], dgate [T] or [H]
- *     float32 (each may be NULL; overwritten).  dx may be dout, dadd or x.
+ *     float32 (each may be NULL; overwritten).  dx may be dout, dadd or x
+ *     (the same pointer; other overlaps: MOE_ERR_INVALID_ARG).
  *   Row statistics are recomputed from x.  Deterministic.  Workspace:
  *   moe_norm_backward_workspace_size() bytes, 16-byte aligned.
  *

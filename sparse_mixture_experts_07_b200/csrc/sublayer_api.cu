@@ -46,6 +46,23 @@ template <size_t N> bool all_aligned(const void* const (&ptrs)[N]) {
     return true;
 }
 
+// Buffers of a call.  A row's values are read before they are written by the
+// same thread, so an output may be an input of its size; anything else that
+// shares memory with it is refused.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+bool apart(const Span& a, const Span& b) {
+    const auto x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return !a.p || !b.p || x + a.bytes <= y || y + b.bytes <= x;
+}
+bool same_or_apart(const Span& a, const Span& b) { return a.p == b.p || apart(a, b); }
+
+Span rows_span(const moe_shape* s, const void* p, int64_t rows) {
+    return {p, static_cast<size_t>(rows) * static_cast<size_t>(s->H) * elem_bytes(*s)};
+}
+
 struct Interval {
     uintptr_t begin, end;
     bool operator<(const Interval& o) const { return begin < o.begin; }
@@ -162,6 +179,8 @@ moe_status moe_norm_forward(const moe_shape* shape, const moe_norm_spec* norm, c
     const bool vec = all_aligned(ptrs) && p.H % 4 == 0;
     const bool bf16 = shape->dtype == MOE_BF16;
     if (bf16 && !vec) return MOE_ERR_UNSUPPORTED;
+    if (!same_or_apart(rows_span(shape, y, p.T), rows_span(shape, x, p.T)))
+        return MOE_ERR_INVALID_ARG;
     return cuda_status(moe::launch_combine_norm(p, bf16, vec, num_sms(),
                                                 static_cast<cudaStream_t>(stream)));
 }
@@ -200,6 +219,15 @@ moe_status moe_combine_norm(const moe_shape* shape, const void* y_slots, const i
     const bool vec = all_aligned(ptrs) && p.H % 4 == 0;
     const bool bf16 = shape->dtype == MOE_BF16;
     if (bf16 && !vec) return MOE_ERR_UNSUPPORTED;
+    const Span slots = rows_span(shape, y_slots, p.T * (p.k + p.S));
+    const Span res = rows_span(shape, residual, p.T);
+    const Span outs[] = {rows_span(shape, h_out, p.T), rows_span(shape, xn_out, p.T),
+                         rows_span(shape, y_out, p.T)};
+    for (int i = 0; i < 3; ++i) {
+        if (!apart(outs[i], slots) || !same_or_apart(outs[i], res)) return MOE_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (!apart(outs[i], outs[j])) return MOE_ERR_INVALID_ARG;
+    }
     return cuda_status(moe::launch_combine_norm(p, bf16, vec, num_sms(),
                                                 static_cast<cudaStream_t>(stream)));
 }
@@ -252,6 +280,9 @@ moe_status moe_norm_backward(const moe_shape* shape, const moe_norm_spec* norm, 
     const bool vec = all_aligned(ptrs) && p.H % 4 == 0;
     const bool bf16 = shape->dtype == MOE_BF16;
     if (bf16 && !vec) return MOE_ERR_UNSUPPORTED;
+    const Span out = rows_span(shape, dx, p.T);
+    for (const void* in : {x, dout, dadd})
+        if (!same_or_apart(out, rows_span(shape, in, p.T))) return MOE_ERR_INVALID_ARG;
     return cuda_status(moe::launch_norm_backward(p, bf16, vec, num_sms(),
                                                  static_cast<cudaStream_t>(stream)));
 }

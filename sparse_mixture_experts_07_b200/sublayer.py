@@ -146,7 +146,7 @@ def combine_norm(shape: Shape, y_slots, inv, residual=None, post: Optional[Norm]
 
     gate: [T, 1] (per token) or [H] (per channel) float32.  keep_y: also return
     y (rounded), which norm_backward reads.  out: optional dict of h, xn, y
-    buffers (h may be `residual`)."""
+    buffers, apart from one another (one of them may be `residual`)."""
     lib, dev, dt = load_library(), _cuda(y_slots), shape.torch_dtype
     size = (shape.T, shape.H)
     _tensor("y_slots", y_slots, (shape.slot_rows, shape.H), dt, dev)
@@ -161,6 +161,8 @@ def combine_norm(shape: Shape, y_slots, inv, residual=None, post: Optional[Norm]
         _check_norm("next_norm", next_norm, shape.H, dev)
     kind = _gate_kind(gate, shape, dev)
     bufs = dict(out) if out else {}
+    if not bufs.keys() <= {"h", "xn", "y"}:
+        raise ValueError(f"out takes buffers named h, xn and y, got {sorted(bufs)}")
     for name, t in bufs.items():
         if t is not None:
             _tensor(name, t, size, dt, dev)

@@ -802,3 +802,64 @@ def test_clip_without_a_limit_only_measures(cuda_ok, bad):
         else:
             assert got[0][4321].isnan() and not got[1].any() and not got[2].any()
             assert not got[0][:4321].any() and not got[0][4322:].any()
+
+
+def test_overlapping_buffers_are_refused(lib):
+    """Outputs that share memory with one another or with the slots, or with an
+    input's rows at another offset, are refused before any launch."""
+    spec = ctypes.byref(MoENormSpec(1, 1e-5, None, None))
+    row, size = 128 * 2, 4 * 128 * 2                 # bytes of a row, of T = 4 rows
+    slots, inv, res, h, xn, y = (1 << 20, 1 << 24, 2 << 20, 3 << 20, 4 << 20, 5 << 20)
+
+    def f(h=h, xn=xn, y=y):
+        return lib.moe_combine_norm(_c(), slots, inv, res, spec, 0, None, 1.0, spec, y, h, xn,
+                                    None)
+    assert f(xn=h) == 1 and f(y=h) == 1 and f(y=xn) == 1
+    assert f(xn=h + size - row) == 1 and f(y=h - row) == 1
+    assert f(h=slots) == 1 and f(xn=slots + 7 * row) == 1 and f(y=slots - size + row) == 1
+    assert f(h=res + row) == 1 and f(xn=res - row) == 1 and f(y=res + size - 16) == 1
+    assert f(h=res, y=res) == 1
+
+    assert lib.moe_norm_forward(_c(), spec, res, res + row, None) == 1
+    assert lib.moe_norm_forward(_c(), spec, res, res - size + 16, None) == 1
+    n = ctypes.c_size_t(0)
+    assert lib.moe_norm_backward_workspace_size(_c(), ctypes.byref(n)) == 0
+
+    def b(x=res, dout=h, dadd=y, dx=xn):
+        return lib.moe_norm_backward(_c(), spec, x, dout, 0, None, 1.0, dadd, dx, None, None,
+                                     None, inv, n.value, None)
+    assert b(dx=res + row) == 1 and b(dx=h - row) == 1 and b(dx=y + size - row) == 1
+
+
+def test_unknown_output_names_are_refused(lib):
+    class Device(torch.Tensor):
+        is_cuda = True
+    t = torch.zeros(8, 128, dtype=torch.bfloat16).as_subclass(Device)
+    with pytest.raises(ValueError, match="h, xn and y"):
+        moe.combine_norm(_shape(4, 128), t, torch.zeros(8, dtype=torch.int32), out={"hn": t[:4]})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,H", [(torch.bfloat16, 264), (torch.float32, 131)])
+def test_outputs_in_place_of_inputs(cuda_ok, dtype, H):
+    """Each output in the residual's place, N(x) in x's and dx in any input's:
+    the values of separate buffers."""
+    T = 300
+    g, slots, inv, res = _forward_inputs(T, H, 2, 0, dtype)
+    s = _shape(T, H, dtype=dtype)
+    spec, _ = _params(g, "layer", H)
+    slots, inv, res = slots.cuda(), inv.cuda(), res.cuda()
+    want = moe.combine_norm(s, slots, inv, res, post=spec, next_norm=spec, keep_y=True)
+    for i, name in enumerate(("h", "xn", "y")):
+        place = res.clone()
+        got = moe.combine_norm(s, slots, inv, place, post=spec, next_norm=spec, keep_y=True,
+                               out={name: place})
+        assert got[i].data_ptr() == place.data_ptr()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    place = res.clone()
+    assert torch.equal(moe.norm(s, spec, place, out=place), moe.norm(s, spec, res))
+    ins = dict(x=res, dout=want[0], dadd=want[1])
+    dx = moe.norm_backward(s, spec, **ins)["x"]
+    for name in ins:
+        place = ins[name].clone()
+        assert torch.equal(moe.norm_backward(s, spec, **{**ins, name: place}, dx=place)["x"], dx)
