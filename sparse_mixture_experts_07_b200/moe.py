@@ -167,18 +167,19 @@ def alloc_workspace(shape: Shape, device="cuda") -> torch.Tensor:
     return torch.empty(max(workspace_size(shape), 1), dtype=torch.uint8, device=device)
 
 
-def router_split(shape: Shape, w_router, stream=None):
+def router_split(shape: Shape, w_router, stream=None, out=None):
     """The router weight split into three bf16 terms [N, H] (hi, mid, lo planes of
     E_PAD rows each, zero padding), for the tensor-core router; None when that
-    router does not apply to `shape`.  Done once per weight."""
+    router does not apply to `shape`.  Done once per weight.  `out`: an earlier
+    split of this shape to overwrite."""
     lib = load_library()
     n = ctypes.c_size_t(0)
     _check(lib.moe_router_split_size(ctypes.byref(shape.c()), ctypes.byref(n)),
            "moe_router_split_size")
     if n.value == 0:
         return None
-    ws = torch.empty(n.value // (2 * shape.H), shape.H, dtype=torch.bfloat16,
-                     device=w_router.device)
+    ws = out if out is not None else torch.empty(
+        n.value // (2 * shape.H), shape.H, dtype=torch.bfloat16, device=w_router.device)
     _check(lib.moe_router_split(ctypes.byref(shape.c()), _ptr(w_router), _ptr(ws), n.value,
                                 _stream(stream)), "moe_router_split")
     return ws
@@ -464,7 +465,8 @@ class MoELayer:
     experts are merged at construction into one of their summed width
     (moe_shared_merge): `self.shape` and `self.sh_gate_up` / `self.sh_down`
     are then the merged ones the library calls run on, and y_slots holds one
-    shared row per token.
+    shared row per token.  The router weight is split at construction: after
+    changing `w_router` in place, call refresh_router().
     """
 
     def __init__(self, shape: Shape, w_router, router_bias, gate_up=None, down=None,
@@ -488,7 +490,7 @@ class MoELayer:
         if routing is not None and routing[0] != "noaux_tc":
             raise ValueError(f"unknown routing {routing!r}")
         self.w_router, self.router_bias = w_router, router_bias
-        # split once here, at load time; refresh it if w_router changes
+        # split once here, at load time; see refresh_router
         self.w_split = router_split(shape, w_router)
         self.gate_up, self.down = gate_up, down
         self.sh_gate_up, self.sh_down = sh_gate_up, sh_down
@@ -523,6 +525,12 @@ class MoELayer:
         if routing is not None:
             self.buf["logits"] = torch.empty(T, E, dtype=torch.float32, device=dev)
         self.last = None
+
+    def refresh_router(self, stream=None):
+        """Splits w_router again after it changed in place, into the buffer that
+        calls and captured graphs of this layer read."""
+        if self.w_split is not None:
+            router_split(self.shape, self.w_router, stream=stream, out=self.w_split)
 
     def slots(self, x, stream=None):
         """The step up to the combine: (y_slots, inv), this layer's buffers."""

@@ -317,6 +317,10 @@ class MoESublayer:
 
     `gate` [T, 1] or [H] float32, or None.  __call__ is the serving form;
     forward_train / backward the training form (bf16, more than 8 tokens).
+    The weights may change in place from step to step.  Serving after such a
+    change: layer.refresh_router() first.  A layer that merged its shared experts
+    is trained on the merged layer.sh_gate_up and layer.sh_down, whose shapes
+    their gradients have (merge_shared=False keeps them as given).
     """
 
     def __init__(self, layer: MoELayer, pre: Norm, post: Optional[Norm] = None, gate=None,
@@ -345,6 +349,7 @@ class MoESublayer:
             raise ValueError("training needs bf16 expert weights and the softmax routing")
         dev = h.device
         xn = norm(s, self.pre, h)
+        layer.refresh_router()           # the last step changed the weight
         idx, w, logits = _moe.route(s, xn, layer.w_router, layer.router_bias, logits=True,
                                     err_flag=layer.err_flag, w_split=layer.w_split)
         counts, offsets, perm, inv = _moe.permute(s, idx, layer.workspace, layer.err_flag)

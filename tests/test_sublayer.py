@@ -863,3 +863,34 @@ def test_outputs_in_place_of_inputs(cuda_ok, dtype, H):
     for name in ins:
         place = ins[name].clone()
         assert torch.equal(moe.norm_backward(s, spec, **{**ins, name: place}, dx=place)["x"], dx)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [100, 300])
+def test_training_steps_route_by_the_weight_they_find(cuda_ok, T):
+    """The router's weight changes in place between steps, as an optimiser leaves
+    it: each step's selection and outputs are a fresh layer's, and after
+    refresh_router the serving form's and a captured graph's are too."""
+    cfg = MoEConfig("steps", T=T, H=128, I=96, E=4, k=2, n_shared=1, I_shared=64)
+    _, sub, h, _, _ = _sublayer(cfg)
+    layer, h = sub.layer, h.cuda()
+    graph = layer.capture(moe.norm(layer.shape, sub.pre, h))
+    for step in range(3):
+        layer.w_router.copy_(layer.w_router.roll(1, 0) * 1.25)
+        fresh = moe.MoELayer(layer.shape, layer.w_router.clone(), layer.router_bias,
+                             layer.gate_up, layer.down, layer.sh_gate_up, layer.sh_down,
+                             merge_shared=False)
+        again = moe.MoESublayer(fresh, sub.pre, sub.post, None, sub.scale, sub.next_norm)
+        h2, saved = sub.forward_train(h)
+        want, w_saved = again.forward_train(h)
+        assert torch.equal(saved["topk_idx"], w_saved["topk_idx"])
+        assert torch.equal(saved["logits"], w_saved["logits"]) and torch.equal(h2, want)
+        layer.w_router.copy_(layer.w_router.flip(0))
+        fresh.w_router.copy_(layer.w_router)
+        fresh = moe.MoELayer(layer.shape, fresh.w_router, layer.router_bias, layer.gate_up,
+                             layer.down, layer.sh_gate_up, layer.sh_down, merge_shared=False)
+        layer.refresh_router()
+        want = fresh(graph.x).clone()
+        assert torch.equal(layer(graph.x), want)
+        layer.buf["y"].zero_()
+        assert torch.equal(graph.replay(), want)
