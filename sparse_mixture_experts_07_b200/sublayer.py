@@ -315,7 +315,8 @@ class MoESublayer:
 
         h' = h + scale * gate * N_post(block(N_pre(h)))      (and N_next(h'))
 
-    `gate` [T, 1] or [H] float32, or None.  __call__ is the serving form;
+    `gate` [T, 1] or [H] float32, or None; a gate that depends on the tokens is
+    given to the call instead.  __call__ is the serving form;
     forward_train / backward the training form (bf16, more than 8 tokens).
     The weights may change in place from step to step.  Serving after such a
     change: layer.refresh_router() first.  A layer that merged its shared experts
@@ -330,21 +331,24 @@ class MoESublayer:
         self.xn = torch.empty(layer.shape.T, layer.shape.H, dtype=layer.shape.torch_dtype,
                               device=layer.err_flag.device)
 
-    def __call__(self, h, xn=None, out=None, stream=None):
+    def __call__(self, h, xn=None, out=None, stream=None, gate=None):
         """(h', N_next(h') or None).  `xn`: N_pre(h) when the previous layer's
         fused next norm has computed it already.  `out`: optional dict of h and
-        xn buffers."""
+        xn buffers.  `gate`: this call's, in place of the sub-layer's."""
         layer = self.layer
         if xn is None:
             xn = norm(layer.shape, self.pre, h, out=self.xn, stream=stream)
         y_slots, inv = layer.slots(xn, stream=stream)
-        return combine_norm(layer.shape, y_slots, inv, h, post=self.post, gate=self.gate,
+        return combine_norm(layer.shape, y_slots, inv, h, post=self.post,
+                            gate=self.gate if gate is None else gate,
                             scale=self.scale, next_norm=self.next_norm, out=out,
                             stream=stream)[:2]
 
-    def forward_train(self, h):
-        """(h', saved): the training forward; `saved` is what backward reads."""
+    def forward_train(self, h, gate=None):
+        """(h', saved): the training forward; `saved` is what backward reads, the
+        step's norms, gate and scale among it.  `gate` as in __call__."""
         layer, s = self.layer, self.layer.shape
+        gate = self.gate if gate is None else gate
         if layer.gate_up is None or layer.routing is not None:
             raise ValueError("training needs bf16 expert weights and the softmax routing")
         dev = h.device
@@ -357,9 +361,10 @@ class MoESublayer:
         y_slots = _moe.forward_train(s, xn, offsets, perm, w, layer.gate_up, layer.down,
                                      layer.sh_gate_up, layer.sh_down, layer.workspace, state,
                                      layer.err_flag)
-        h2, _, y = combine_norm(s, y_slots, inv, h, post=self.post, gate=self.gate,
+        h2, _, y = combine_norm(s, y_slots, inv, h, post=self.post, gate=gate,
                                 scale=self.scale, keep_y=True)
-        return h2, dict(h=h, xn=xn, y=y, topk_idx=idx, topk_w=w, logits=logits, counts=counts,
+        return h2, dict(h=h, xn=xn, y=y, pre=self.pre, post=self.post, gate=gate,
+                        scale=self.scale, topk_idx=idx, topk_w=w, logits=logits, counts=counts,
                         offsets=offsets, perm=perm, inv=inv, state=state)
 
     def backward(self, saved, dh, aux_coef: float = 0.0):
@@ -367,8 +372,8 @@ class MoESublayer:
         (moe.backward's names) and pre_weight, pre_bias, post_weight,
         post_bias, gate (float32; absent where there is none)."""
         layer, s = self.layer, self.layer.shape
-        post = self.post if self.post is not None else Norm("none")
-        gp = norm_backward(s, post, saved["y"], dh, gate=self.gate, scale=self.scale)
+        post = saved["post"] if saved["post"] is not None else Norm("none")
+        gp = norm_backward(s, post, saved["y"], dh, gate=saved["gate"], scale=saved["scale"])
         ws = torch.empty(_moe.backward_workspace_size(s), dtype=torch.uint8, device=dh.device)
         g = _moe.backward(s, saved["xn"], layer.w_router, saved["topk_idx"], saved["topk_w"],
                           saved["counts"], saved["offsets"], saved["perm"], saved["inv"],
@@ -376,7 +381,7 @@ class MoESublayer:
                           saved["state"], gp["x"], ws, layer.err_flag, logits=saved["logits"],
                           aux_coef=aux_coef)
         # the residual's gradient joins in the norm's backward pass
-        gn = norm_backward(s, self.pre, saved["h"], g.pop("x"), dadd=dh)
+        gn = norm_backward(s, saved["pre"], saved["h"], g.pop("x"), dadd=dh)
         g["h"] = gn["x"]
         for name, part in (("pre", gn), ("post", gp)):
             for p in ("weight", "bias"):

@@ -894,3 +894,28 @@ def test_training_steps_route_by_the_weight_they_find(cuda_ok, T):
         assert torch.equal(layer(graph.x), want)
         layer.buf["y"].zero_()
         assert torch.equal(graph.replay(), want)
+
+
+@pytest.mark.gpu
+def test_two_steps_with_gates_of_their_own(cuda_ok):
+    """A gate per token comes with each call; two training steps whose backward
+    passes run after both, as with accumulated micro-batches, and after the
+    sub-layer's own attributes changed, give what each alone gives."""
+    _, sub, h, _, _ = _sublayer(SUB, nxt=False)
+    g = torch.Generator().manual_seed(12)
+    hs = [h.cuda(), (h + 1).cuda()]
+    gates = [torch.rand(SUB.T, 1, generator=g).cuda() for _ in hs]
+    dh = torch.randn(SUB.T, SUB.H, generator=g).to(torch.bfloat16).cuda()
+    alone = []
+    for x, gate in zip(hs, gates):
+        one = moe.MoESublayer(sub.layer, sub.pre, sub.post, gate, sub.scale)
+        h2, saved = one.forward_train(x)
+        alone.append((h2, one.backward(saved, dh), one(x)[0].clone()))
+    steps = [sub.forward_train(x, gate=gate) for x, gate in zip(hs, gates)]
+    served = [sub(x, gate=gate)[0] for x, gate in zip(hs, gates)]
+    sub.gate, sub.scale, sub.post = gates[0].clone().fill_(9.0), 3.0, None
+    for (h2, saved), y, (want, grads, serving) in zip(steps, served, alone):
+        assert torch.equal(h2, want) and torch.equal(y, serving)
+        got = sub.backward(saved, dh)
+        assert set(got) == set(grads) and "gate" in got
+        assert all(torch.equal(got[n], grads[n]) for n in grads)
