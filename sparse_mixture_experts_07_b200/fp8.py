@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from .moe import MOE_BF16, MOE_F32, Shape, _check, load_library
-from .sublayer import _addr, _cuda, _launch, _tensor
+from .sublayer import _addr, _cuda, _launch, _on, _tensor
 
 CODE_TYPES = (torch.float8_e4m3fn, torch.uint8)
 
@@ -67,7 +67,8 @@ def fp8_workspace_size(shape: Shape) -> int:
 
 
 def alloc_fp8_workspace(shape: Shape, device="cuda") -> torch.Tensor:
-    return torch.empty(max(fp8_workspace_size(shape), 1), dtype=torch.uint8, device=device)
+    with _on(device):
+        return torch.empty(max(fp8_workspace_size(shape), 1), dtype=torch.uint8, device=device)
 
 
 def _codes(name, t, size, dev):

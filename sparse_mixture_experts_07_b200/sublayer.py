@@ -9,6 +9,7 @@ allocates (outputs, a missing workspace) is allocated on that stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -122,6 +123,12 @@ class _launch:
             self.guard.__exit__(*exc)
 
 
+def _on(device):
+    """`device` current inside: what is sized by its SMs is sized by that device's."""
+    device = torch.device(device)
+    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+
+
 def norm(shape: Shape, spec: Norm, x, out=None, stream=None):
     """N(x) [T, H] (dtype): the norm before the block."""
     lib, dev, size = load_library(), _cuda(x), (shape.T, shape.H)
@@ -195,7 +202,8 @@ def norm_backward_workspace_size(shape: Shape) -> int:
 
 
 def alloc_norm_backward_workspace(shape: Shape, device="cuda") -> torch.Tensor:
-    return torch.empty(norm_backward_workspace_size(shape), dtype=torch.uint8, device=device)
+    with _on(device):
+        return torch.empty(norm_backward_workspace_size(shape), dtype=torch.uint8, device=device)
 
 
 def norm_backward(shape: Shape, spec: Norm, x, dout, gate=None, scale: float = 1.0, dadd=None,

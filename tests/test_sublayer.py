@@ -919,3 +919,28 @@ def test_two_steps_with_gates_of_their_own(cuda_ok):
         got = sub.backward(saved, dh)
         assert set(got) == set(grads) and "gate" in got
         assert all(torch.equal(got[n], grads[n]) for n in grads)
+
+
+def test_workspaces_are_sized_on_their_device(lib, monkeypatch):
+    """The sizes go by the SMs of the current device: the one asked for is current
+    while they are taken."""
+    seen = []
+
+    class Current:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            seen.append(self.device)
+
+        def __exit__(self, *exc):
+            seen.append(None)
+    monkeypatch.setattr(torch.cuda, "device", Current)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: (n, device))
+    for module, size, alloc in (
+            (moe.sublayer, "norm_backward_workspace_size", moe.alloc_norm_backward_workspace),
+            (moe.fp8, "fp8_workspace_size", moe.alloc_fp8_workspace)):
+        seen.clear()
+        monkeypatch.setattr(module, size, lambda shape: seen.append("sized") or 7)
+        assert alloc(_shape(4, 128), "cuda:1") == (7, "cuda:1")
+        assert seen == [torch.device("cuda:1"), "sized", None]
