@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from .moe import MOE_BF16, MOE_F32, Shape, _check, load_library
-from .sublayer import _addr, _cuda, _launch, _on, _tensor
+from .sublayer import _addr, _check_workspace, _cuda, _launch, _nbytes, _on, _tensor
 
 CODE_TYPES = (torch.float8_e4m3fn, torch.uint8)
 
@@ -107,9 +107,11 @@ def forward_fp8(shape: Shape, x, offsets, perm, topk_w, fp8: dict, workspace=Non
     check_fp8_experts(shape, fp8, dev)
     if y_slots is not None:
         _tensor("y_slots", y_slots, (shape.slot_rows, shape.H), shape.torch_dtype, dev)
-    for name, t in (("workspace", workspace), ("err_flag", err_flag)):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the tensors on {dev}")
+    _check_workspace(workspace, dev)
+    if err_flag is not None and (err_flag.device != dev or err_flag.dtype != torch.int32
+                                 or err_flag.numel() < 1):
+        raise ValueError(f"err_flag must be an int32 word on {dev}, got {err_flag.dtype} "
+                         f"{tuple(err_flag.shape)} on {err_flag.device}")
     with _launch(dev, stream) as st:
         if workspace is None:
             workspace = alloc_fp8_workspace(shape, dev)
@@ -121,5 +123,5 @@ def forward_fp8(shape: Shape, x, offsets, perm, topk_w, fp8: dict, workspace=Non
             ctypes.byref(shape.c()), x.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
             topk_w.data_ptr(), fp8["gate_up_q"].data_ptr(), fp8["gate_up_s"].data_ptr(),
             fp8["down_q"].data_ptr(), fp8["down_s"].data_ptr(), *sh, y_slots.data_ptr(),
-            _addr(err_flag), workspace.data_ptr(), workspace.numel(), st), "moe_forward_fp8")
+            _addr(err_flag), workspace.data_ptr(), _nbytes(workspace), st), "moe_forward_fp8")
     return y_slots

@@ -129,6 +129,18 @@ def _on(device):
     return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
 
 
+def _check_workspace(t, device):
+    """Kernels write the workspace as one run of bytes from its first."""
+    if t is not None and t.device != device:
+        raise ValueError(f"workspace is on {t.device}, the tensors on {device}")
+    if t is not None and not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous, got strides {t.stride()}")
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
 def norm(shape: Shape, spec: Norm, x, out=None, stream=None):
     """N(x) [T, H] (dtype): the norm before the block."""
     lib, dev, size = load_library(), _cuda(x), (shape.T, shape.H)
@@ -218,8 +230,7 @@ def norm_backward(shape: Shape, spec: Norm, x, dout, gate=None, scale: float = 1
             _tensor(name, t, size, dt, dev)
     _check_norm("norm", spec, shape.H, dev)
     kind = _gate_kind(gate, shape, dev)
-    if workspace is not None and workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the tensors on {dev}")
+    _check_workspace(workspace, dev)
     with _launch(dev, stream) as s:
         if workspace is None:
             workspace = alloc_norm_backward_workspace(shape, dev)
@@ -230,8 +241,8 @@ def norm_backward(shape: Shape, spec: Norm, x, dout, gate=None, scale: float = 1
         _check(lib.moe_norm_backward(
             ctypes.byref(shape.c()), ctypes.byref(spec.c()), x.data_ptr(), dout.data_ptr(), kind,
             _addr(gate), scale, _addr(dadd), g["x"].data_ptr(), _addr(g["weight"]), _addr(g["bias"]),
-            _addr(g["gate"]), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            s), "moe_norm_backward")
+            _addr(g["gate"]), workspace.data_ptr(), _nbytes(workspace), s),
+            "moe_norm_backward")
     return g
 
 
@@ -271,8 +282,7 @@ def _grad_arrays(grads):
 def _check_clip(dev, workspace=None):
     if dev is None:
         raise ValueError("no gradients given")
-    if workspace is not None and workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the gradients on {dev}")
+    _check_workspace(workspace, dev)
 
 
 def grad_square_sum(grads: Sequence[Optional[torch.Tensor]], workspace=None, stream=None):
@@ -285,7 +295,7 @@ def grad_square_sum(grads: Sequence[Optional[torch.Tensor]], workspace=None, str
         ws = alloc_grad_norm_workspace(dev) if workspace is None else workspace
         total = torch.empty(1, dtype=torch.float64, device=dev)
         _check(lib.moe_grad_square_sum(n, ptrs, sizes, types, total.data_ptr(), ws.data_ptr(),
-                                       ws.numel(), s), "moe_grad_square_sum")
+                                       _nbytes(ws), s), "moe_grad_square_sum")
     return total
 
 
@@ -313,7 +323,7 @@ def clip_grad_norm(grads, max_norm: float, workspace=None, stream=None):
         ws = alloc_grad_norm_workspace(dev) if workspace is None else workspace
         norm_out = torch.empty(1, dtype=torch.float32, device=dev)
         _check(lib.moe_clip_grad_norm(n, ptrs, sizes, types, max_norm, norm_out.data_ptr(),
-                                      ws.data_ptr(), ws.numel(), s), "moe_clip_grad_norm")
+                                      ws.data_ptr(), _nbytes(ws), s), "moe_clip_grad_norm")
     return norm_out
 
 

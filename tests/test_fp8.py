@@ -563,3 +563,26 @@ def test_holes_are_zero_on_any_workspace(cuda_ok, T, fill):
     keep = torch.ones(shape.slot_rows, dtype=torch.bool, device="cuda")
     keep[rows] = False
     assert torch.equal(got[keep], y[keep]) and (got[~keep] == 0).all()
+
+
+@pytest.mark.gpu
+def test_workspace_and_error_word_refusals(cuda_ok):
+    shape, x, perm, offsets, w, fp8 = _setup(5, 144, 272, 4, 2, 0, 0, seed=16)
+    want = _run(shape, x, perm, offsets, w, fp8)
+    n = moe.fp8_workspace_size(shape)
+    got = _run(shape, x, perm, offsets, w, fp8,
+               workspace=torch.empty(n // 4 + 1, dtype=torch.int32, device="cuda"))
+    assert torch.equal(got, want)
+    dev = [t.cuda() for t in (x, offsets, perm, w)] + [{m: t.cuda() for m, t in fp8.items()}]
+    for kw, match in (
+            (dict(workspace=torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]),
+             "contiguous"),
+            (dict(workspace=torch.empty(n, dtype=torch.uint8)), "workspace is on cpu"),
+            (dict(err_flag=torch.zeros(1, device="cuda")), "err_flag"),
+            (dict(err_flag=torch.zeros(1, dtype=torch.int32)), "err_flag"),
+            (dict(err_flag=torch.zeros(0, dtype=torch.int32, device="cuda")), "err_flag")):
+        with pytest.raises(ValueError, match=match):
+            moe.forward_fp8(shape, *dev, **kw)
+    with pytest.raises(moe.MoEError, match="WORKSPACE"):
+        moe.forward_fp8(shape, *dev, workspace=torch.empty(n - 1, dtype=torch.uint8,
+                                                           device="cuda"))

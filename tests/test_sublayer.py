@@ -944,3 +944,38 @@ def test_workspaces_are_sized_on_their_device(lib, monkeypatch):
         monkeypatch.setattr(module, size, lambda shape: seen.append("sized") or 7)
         assert alloc(_shape(4, 128), "cuda:1") == (7, "cuda:1")
         assert seen == [torch.device("cuda:1"), "sized", None]
+
+
+def test_workspaces_are_one_run_of_bytes():
+    """A strided view spans memory that is not its own."""
+    check, cpu = moe.sublayer._check_workspace, torch.device("cpu")
+    check(None, cpu)
+    check(torch.zeros(64, dtype=torch.uint8), cpu)
+    with pytest.raises(ValueError, match="contiguous"):
+        check(torch.zeros(64, dtype=torch.uint8)[::2], cpu)
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        check(torch.zeros(64, dtype=torch.uint8), torch.device("cuda:0"))
+
+
+@pytest.mark.gpu
+def test_workspaces_of_any_type(cuda_ok):
+    """Bytes count, whatever the element; one too short, or strided, is refused."""
+    T, H = 40, 264
+    s, g = _shape(T, H), torch.Generator().manual_seed(2)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()
+    spec, _ = _params(g, "rms", H)
+    want = moe.norm_backward(s, spec, x, x)
+    n = moe.norm_backward_workspace_size(s)
+    got = moe.norm_backward(s, spec, x, x, workspace=torch.empty(n // 4, device="cuda"))
+    assert torch.equal(got["weight"], want["weight"])
+    grads = [x.clone()]
+    for m in (moe.alloc_grad_norm_workspace().numel(),):
+        ws = torch.empty(m // 8, dtype=torch.float64, device="cuda")
+        assert torch.equal(moe.clip_grad_norm(grads, 1e9, workspace=ws),
+                           moe.clip_grad_norm(grads, 1e9))
+        assert torch.equal(moe.grad_square_sum(grads, workspace=ws), moe.grad_square_sum(grads))
+        with pytest.raises(moe.MoEError, match="WORKSPACE"):
+            moe.clip_grad_norm(grads, 1.0, workspace=ws[1:])
+        with pytest.raises(ValueError, match="contiguous"):
+            moe.clip_grad_norm(grads, 1.0, workspace=torch.empty(2 * m, dtype=torch.uint8,
+                                                                 device="cuda")[::2])
