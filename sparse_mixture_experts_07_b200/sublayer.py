@@ -354,19 +354,23 @@ class MoESublayer:
         fused next norm has computed it already.  `out`: optional dict of h and
         xn buffers.  `gate`: this call's, in place of the sub-layer's."""
         layer = self.layer
-        if xn is None:
-            xn = norm(layer.shape, self.pre, h, out=self.xn, stream=stream)
-        y_slots, inv = layer.slots(xn, stream=stream)
-        return combine_norm(layer.shape, y_slots, inv, h, post=self.post,
-                            gate=self.gate if gate is None else gate,
-                            scale=self.scale, next_norm=self.next_norm, out=out,
-                            stream=stream)[:2]
+        with _launch(layer.err_flag.device, stream):     # the block's calls follow it
+            if xn is None:
+                xn = norm(layer.shape, self.pre, h, out=self.xn, stream=stream)
+            y_slots, inv = layer.slots(xn, stream=stream)
+            return combine_norm(layer.shape, y_slots, inv, h, post=self.post,
+                                gate=self.gate if gate is None else gate,
+                                scale=self.scale, next_norm=self.next_norm, out=out,
+                                stream=stream)[:2]
 
     def forward_train(self, h, gate=None):
         """(h', saved): the training forward; `saved` is what backward reads, the
         step's norms, gate and scale among it.  `gate` as in __call__."""
+        with _launch(self.layer.err_flag.device, None):
+            return self._forward_train(h, self.gate if gate is None else gate)
+
+    def _forward_train(self, h, gate):
         layer, s = self.layer, self.layer.shape
-        gate = self.gate if gate is None else gate
         if layer.gate_up is None or layer.routing is not None:
             raise ValueError("training needs bf16 expert weights and the softmax routing")
         dev = h.device
@@ -389,6 +393,10 @@ class MoESublayer:
         """Gradients given dh = dL/dh': dict of h (dtype), the block's
         (moe.backward's names) and pre_weight, pre_bias, post_weight,
         post_bias, gate (float32; absent where there is none)."""
+        with _launch(self.layer.err_flag.device, None):
+            return self._backward(saved, dh, aux_coef)
+
+    def _backward(self, saved, dh, aux_coef):
         layer, s = self.layer, self.layer.shape
         post = saved["post"] if saved["post"] is not None else Norm("none")
         gp = norm_backward(s, post, saved["y"], dh, gate=saved["gate"], scale=saved["scale"])

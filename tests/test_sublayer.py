@@ -979,3 +979,48 @@ def test_workspaces_of_any_type(cuda_ok):
         with pytest.raises(ValueError, match="contiguous"):
             moe.clip_grad_norm(grads, 1.0, workspace=torch.empty(2 * m, dtype=torch.uint8,
                                                                  device="cuda")[::2])
+
+
+def test_sublayer_runs_on_its_layers_device(monkeypatch):
+    """Each form makes the layer's device (and the stream given) current around
+    the block's calls, which go by what is current."""
+    from types import SimpleNamespace
+    from sparse_mixture_experts_07_b200 import sublayer
+    seen, inside = [], []
+
+    class Launch:
+        def __init__(self, device, stream):
+            self.args = (device, stream)
+
+        def __enter__(self):
+            inside.append(self.args)
+
+        def __exit__(self, *exc):
+            inside.pop()
+
+    def call(name, result):
+        def f(*args, **kw):
+            seen.append((name, inside[-1] if inside else None))
+            return result
+        return f
+    t = torch.zeros(1, dtype=torch.int32)
+    block = SimpleNamespace(
+        route=call("route", (t, t, t)), permute=call("permute", (t, t, t, t)),
+        train_state_size=lambda s: 1, forward_train=call("forward_train", t),
+        backward_workspace_size=lambda s: 1, backward=call("backward", {"x": t}))
+    monkeypatch.setattr(sublayer, "_launch", Launch)
+    monkeypatch.setattr(sublayer, "_moe", block)
+    monkeypatch.setattr(sublayer, "norm", call("norm", t))
+    monkeypatch.setattr(sublayer, "combine_norm", call("combine_norm", (t, t, t)))
+    monkeypatch.setattr(sublayer, "norm_backward", call(
+        "norm_backward", dict(x=t, weight=None, bias=None, gate=None)))
+    layer = SimpleNamespace(shape=_shape(1, 8), err_flag=t, slots=call("slots", (t, t)),
+                            refresh_router=call("refresh_router", None), gate_up=t, down=t,
+                            routing=None, w_router=t, router_bias=t, w_split=None, workspace=t,
+                            sh_gate_up=None, sh_down=None)
+    sub = moe.MoESublayer(layer, moe.Norm())
+    sub(t, stream="a stream")
+    assert seen == [(n, (t.device, "a stream")) for n in ("norm", "slots", "combine_norm")]
+    seen.clear()
+    sub.backward(sub.forward_train(t)[1], t)
+    assert len(seen) == 9 and all(at == (t.device, None) for _, at in seen)
