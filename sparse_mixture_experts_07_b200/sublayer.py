@@ -354,6 +354,9 @@ class MoESublayer:
         fused next norm has computed it already.  `out`: optional dict of h and
         xn buffers.  `gate`: this call's, in place of the sub-layer's."""
         layer = self.layer
+        for name, t in (("h", h), ("xn", xn)):           # the block reads them unchecked
+            if t is not None:
+                _tensor(name, t, self.xn.shape, self.xn.dtype, self.xn.device)
         with _launch(layer.err_flag.device, stream):     # the block's calls follow it
             if xn is None:
                 xn = norm(layer.shape, self.pre, h, out=self.xn, stream=stream)

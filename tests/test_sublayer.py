@@ -1019,8 +1019,22 @@ def test_sublayer_runs_on_its_layers_device(monkeypatch):
                             routing=None, w_router=t, router_bias=t, w_split=None, workspace=t,
                             sh_gate_up=None, sh_down=None)
     sub = moe.MoESublayer(layer, moe.Norm())
-    sub(t, stream="a stream")
+    h = torch.zeros(1, 8, dtype=torch.bfloat16)
+    sub(h, stream="a stream")
     assert seen == [(n, (t.device, "a stream")) for n in ("norm", "slots", "combine_norm")]
     seen.clear()
-    sub.backward(sub.forward_train(t)[1], t)
+    sub.backward(sub.forward_train(h)[1], h)
     assert len(seen) == 9 and all(at == (t.device, None) for _, at in seen)
+
+
+def test_sublayer_checks_what_the_block_reads():
+    """`xn` goes to the block as a bare pointer."""
+    from types import SimpleNamespace
+    t = torch.zeros(1, dtype=torch.int32)
+    sub = moe.MoESublayer(SimpleNamespace(shape=_shape(4, 64), err_flag=t), moe.Norm())
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for bad in (x[:3], x.float(), torch.zeros(64, 4, dtype=torch.bfloat16).t(), x[:, :32]):
+        with pytest.raises(ValueError, match="xn must be"):
+            sub(x, xn=bad)
+        with pytest.raises(ValueError, match="h must be"):
+            sub(bad)
