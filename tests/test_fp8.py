@@ -586,3 +586,38 @@ def test_workspace_and_error_word_refusals(cuda_ok):
     with pytest.raises(moe.MoEError, match="WORKSPACE"):
         moe.forward_fp8(shape, *dev, workspace=torch.empty(n - 1, dtype=torch.uint8,
                                                            device="cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 24, 96, 400])
+def test_fine_grained_layer_with_noaux_routing(cuda_ok, T):
+    """64 experts, top-6 by groups, two shared experts: the layer on E4M3 weights
+    against the oracle on the device's plan; then a token of NaN, which stays in
+    its row (up to 32 tokens the others' sums are cut at other places: TOL)."""
+    H, I, E, k, S, Is = 256, 96, 64, 6, 2, 128
+    g = torch.Generator().manual_seed(17)
+    fp8 = _experts(g, H, E, I)
+    fp8.update(_experts(g, H, S, Is, "sh_"))
+    dev = {n: t.cuda() for n, t in fp8.items()}
+    shape = moe.Shape(T=T, H=H, I=I, E=E, k=k, n_shared=S, I_shared=Is, routed_scale=2.5)
+    layer = moe.MoELayer(shape, torch.randn(E, H, generator=g).cuda(),
+                         (torch.randn(E, generator=g) * 0.1).cuda(), fp8=dev,
+                         routing=("noaux_tc", 8, 4))
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16)
+    y = layer(x.cuda(), y=torch.empty(T, H, dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
+    assert layer.device_error() == 0
+    b = {n: layer.last[n].cpu() for n in ("perm", "offsets", "topk_w", "inv")}
+    slots = _oracle(shape, x, b["perm"], b["offsets"], b["topk_w"], fp8)
+    want = ref_sub.combine(slots, b["inv"].numpy(), T, k, S)
+    assert rel_l2(y.double().cpu().numpy(), want) <= 2 * TOL       # slots, then y, rounded
+    x[T // 2] = float("nan")
+    got = layer(x.cuda(), y=torch.empty(T, H, dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
+    assert layer.device_error() == 0 and got[T // 2].isnan().all()
+    others = torch.arange(T, device="cuda") != T // 2
+    if T > 32:
+        assert torch.equal(got[others], y[others])
+    elif T > 1:
+        assert rel_l2(got[others].double().cpu().numpy(),
+                      want[others.cpu().numpy()]) <= 2 * TOL
