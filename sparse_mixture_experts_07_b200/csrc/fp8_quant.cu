@@ -13,8 +13,9 @@ namespace {
 // over the CTA's maximum, and its code written once.  A thread holds pieces of
 // 16 columns (bf16: four, of two 16-byte loads each; float32: two, of four), so
 // that a code store is 16 bytes and 1024 resident threads keep 128 KB of loads
-// in flight on an SM.  32 x 6400 x 4096 bf16 (2.5 GB): 392 us, 0.99 of the copy
-// bandwidth; with a division per value the arithmetic took 785 us.
+// in flight on an SM.  32 x 6400 x 4096 bf16 (2.5 GB): 392 to 433 us from card to
+// card, 0.90 to 0.99 of the copy bandwidth; with a division per value the
+// arithmetic took 785 us.
 template <typename T> struct QuantPiece;
 template <> struct QuantPiece<__nv_bfloat16> {
     static constexpr int LOADS = 2, PIECES = 4;

@@ -19,10 +19,11 @@
 // one row at a time; what hides a row's load latency and its block-wide sums is
 // the other CTAs of the SM, so registers are held to five CTAs of 256 threads:
 // two 16-byte vectors per thread and at most 8 loads in flight.  Measured on a
-// B200, 32768 tokens of 2048 columns, 6 + 1 slots (1.34 GB): 230 us, 0.90 of the
-// copy bandwidth.  One vector per thread: 260 us (twice the threads in every
-// barrier); 88 registers and two CTAs less: 316 us; rows copied to shared memory
-// two to four tokens ahead, two CTAs per SM: 303 us and more.
+// B200, 32768 tokens of 2048 columns, 6 + 1 slots (1.34 GB): 230 to 245 us from
+// card to card, 0.85 to 0.90 of the copy bandwidth.  On the card with 230, one
+// vector per thread: 260 us (twice the threads in every barrier); 88 registers and
+// two CTAs less: 316 us; rows copied to shared memory two to four tokens ahead,
+// two CTAs per SM: 303 us and more.
 #include "norm.cuh"
 
 namespace moe {
@@ -45,7 +46,6 @@ template <> struct RowIO<__nv_bfloat16, 8> {
         return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
-    __device__ __forceinline__ static Raw zero() { return make_uint4(0, 0, 0, 0); }
 };
 template <> struct RowIO<float, 4> {
     using Raw = float4;
@@ -55,16 +55,15 @@ template <> struct RowIO<float, 4> {
     __device__ __forceinline__ static Raw pack(const float (&v)[4]) {
         return make_float4(v[0], v[1], v[2], v[3]);
     }
-    __device__ __forceinline__ static Raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 };
 template <> struct RowIO<float, 1> {
     using Raw = float;
     __device__ __forceinline__ static void unpack(const Raw& u, float (&v)[1]) { v[0] = u; }
     __device__ __forceinline__ static Raw pack(const float (&v)[1]) { return v[0]; }
-    __device__ __forceinline__ static Raw zero() { return 0.f; }
 };
 
-// A load, zero when !ok: volatile PTX, so that a group of them stays ahead of the arithmetic: all of the group are in flight together.
+// A load, zero when !ok: volatile PTX, so that a group of them stays ahead of the
+// arithmetic and all of the group are in flight together.
 __device__ __forceinline__ uint4 load_if(const uint4* p, bool ok) {
     uint4 v;
     asm volatile(

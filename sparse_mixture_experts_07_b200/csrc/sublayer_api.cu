@@ -115,8 +115,10 @@ moe::GradList grad_list(int32_t from, int32_t n, void* const* grads, const int64
     return l;
 }
 
-// Partial sums, one per CTA: enough CTAs to keep every SM's loads in flight,
-// no more than the first launch has chunks.
+// Partial sums, one per CTA: enough CTAs to keep every SM's loads in flight, no
+// more than all tensors together have chunks.  (Every launch of 64 tensors has
+// this many, so that each adds to the same partial sums; a CTA without a chunk
+// leaves its own as it was.)
 int grad_parts(int32_t n, const int64_t* numel, int32_t chunk) {
     int64_t chunks = 0;
     for (int32_t i = 0; i < n; ++i) chunks += (numel[i] + chunk - 1) / chunk;
@@ -151,7 +153,7 @@ moe_status scale_all(int32_t n, void* const* grads, const int64_t* numel, const 
     return MOE_OK;
 }
 
-bool good_max_norm(float m) { return m >= 0.f; }   // infinity: never clips
+bool good_max_norm(float m) { return m >= 0.f; }   // infinity: measures only
 
 }  // namespace
 
