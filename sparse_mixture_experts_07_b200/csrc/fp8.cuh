@@ -122,7 +122,13 @@ struct Fp8Operands {
 
 // Batches whose K-blocks are shared out over the SMs rather than whole tiles:
 // few rows per expert, so that what takes the time is reading the weights, and
-// a tile's sums are small.
+// a tile's sums are small.  Both ways on one B200, us shared out / in whole tiles:
+//                                        1 token  8 tokens  32 tokens  128 tokens
+//   top-2 of 16, 4096 x 6400              42/68    129/146   237/243    257/253
+//   top-8 of 256 + 1, 2048 x 1024         35/33     90/95    200/216    360/354
+//   top-6 of 64 + 2, 2048 x 1024          42/38     80/75    107/93     115/97
+// The rule looks at the tokens alone: the last line's tiles are short and many,
+// and whole ones serve it better throughout.
 constexpr int kFp8SplitRows = 32;      // rows of their tiles
 inline bool fp8_is_split(const moe_shape& s) { return s.T <= kFp8SplitRows; }
 // Batches whose activations are rounded once per token rather than once per

@@ -22,17 +22,16 @@
 // per K-block, and the Mixtral-shaped layer took 3.87 ms against 2.15 ms.
 //
 // Bounds, measured on a B200: 4096 tokens, 8 experts of 4096 x 14336 take
-// 1.71 ms (1.69 PFLOP/s; 2.0 ms at the power cap).  Without the epilogue's work
+// 1.71 to 1.73 ms (1.68 PFLOP/s; 1.94 to 2.05 ms at the power cap; the bf16
+// experts 2.31 and 2.66 ms).  Without the epilogue's work
 // 1.34 ms: a K-block's operands cost one SM 48 KB of shared-memory writes and
 // as many reads.  The rest is the epilogue, 128 multiply-adds per thread and
 // K-block behind the tensor-memory loads.
 //
 // SPLIT (up to 32 tokens): reading the weights is what takes the time, and a
 // tile per CTA leaves SMs idle, so that K-blocks are shared out instead (see
-// Walk).  Experts of 4096 x 6400, top-2 of 16: one token 42 us for 157 MB, 8
-// tokens 127 us, 16 tokens 165 us (whole tiles 192), 32 tokens 193 us (201); at
-// 64 tokens whole tiles are no slower (230 against 232), at 128 faster (233
-// against 271).
+// Walk): one token on two of 16 experts of 4096 x 6400 takes 42 us for 157 MB,
+// in whole tiles 68 us (fp8_is_split has both ways at other sizes).
 #include "fp8.cuh"
 #include "gemm_common.cuh"
 
