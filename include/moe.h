@@ -368,7 +368,9 @@ MOE_API moe_status moe_forward_mxfp4_prepared(const moe_shape* shape, const void
  * reorder the results).  y[t] = sum_j y_slots[inv[t*k+j]]
  *                               + sum_s y_slots[T*k + s*T + t],
  * summed in float32 and rounded once to dtype.
- *   y_slots [T*k + S*T, H] dtype, inv [T*k] int32, y [T, H] dtype output. */
+ *   y_slots [T*k + S*T, H] dtype, inv [T*k] int32, y [T, H] dtype output.
+ * Slots whose entry of inv lies outside [0, T*k) (-1: skipped by moe_permute)
+ * add nothing. */
 MOE_API moe_status moe_combine(const moe_shape* shape, const void* y_slots, const int32_t* inv,
                        void* y, void* stream);
 

@@ -3,10 +3,11 @@
 //   n = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (n + 1e-6)),
 //   g *= c where c < 1
 // (the clipping step of a training loop, over the gradients that moe_backward
-// writes); max_norm = infinity leaves every gradient as it is.  Squares are taken and summed in float64: the square of any float32
-// or bf16 value is a float64 in range, so neither gradients of 1e30 nor of
-// 1e-30 overflow or vanish, and the order of the sum is fixed: chunk by chunk
-// in each thread, threads in a tree, CTAs in order.  No atomics.
+// writes); max_norm = infinity leaves every gradient as it is.  Squares are
+// taken and summed in float64: the square of any float32 or bf16 value is a
+// float64 in range, so neither gradients of 1e30 nor of 1e-30 overflow or
+// vanish, and the order of the sum is fixed: chunk by chunk in each thread,
+// threads in a tree, CTAs in order.  No atomics.
 //
 // Bound by memory: one read for the norm, one read and one write for the
 // scaling (nothing beyond the first read when the norm is within the limit).

@@ -115,3 +115,35 @@ def test_backward_is_deterministic(cuda_ok):
     b = _run(cfg, inp, dy)
     for key in ("x", "gate_up", "down", "sh_gate_up", "sh_down", "w_router", "router_bias"):
         assert torch.equal(a[key], b[key]), key
+
+
+def test_backward_on_a_plan_of_bad_indices(cuda_ok):
+    """Slots whose expert index is out of range are skipped without a read out of
+    range; the tokens that have none get the dx of the whole plan."""
+    import sparse_mixture_experts_07_b200 as moe
+    cfg = MoEConfig("bwd_bad", T=300, H=128, I=96, E=6, k=3)
+    d = to_device(make_inputs(cfg))
+    shape, dy = moe.Shape.from_config(cfg), _dy(cfg).cuda()
+    ws = moe.alloc_workspace(shape)
+    idx, w, logits = moe.route(shape, d["x"], d["w_router"], d["router_bias"], logits=True)
+
+    def run(idx):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        counts, offsets, perm, inv = moe.permute(shape, idx, ws, err)
+        state = torch.zeros(moe.train_state_size(shape), dtype=torch.uint8, device="cuda")
+        moe.forward_train(shape, d["x"], offsets, perm, w, d["gate_up"], d["down"], None, None,
+                          ws, state, err)
+        bws = torch.zeros(moe.backward_workspace_size(shape), dtype=torch.uint8, device="cuda")
+        g = moe.backward(shape, d["x"], d["w_router"], idx, w, counts, offsets, perm, inv,
+                         d["gate_up"], d["down"], None, None, state, dy, bws, err,
+                         logits=logits)
+        torch.cuda.synchronize()
+        return g["x"], err.item()
+    want, err = run(idx)
+    assert err == 0
+    bad = idx.clone()
+    bad[::7, 1], bad[3::11, 0], bad[5::13, 2] = cfg.E, -1, 2 ** 31 - 1
+    healthy = (bad == idx).all(1)
+    assert 0 < int((~healthy).sum()) < cfg.T
+    got, err = run(bad)
+    assert err == 1 << 5 and torch.equal(got[healthy], want[healthy])
